@@ -21,6 +21,12 @@
  *                             the routed experts' SwiGLU FFN (grouped GEMMs)
  *   moe_ep_layout / moe_ep_permute / moe_ep_combine
  *                             expert-parallel exchange over peer memory
+ *   moe_add_rmsnorm           residual addition and RMS norm in front of the gate,
+ *                             with microscaled (MX) rows for the experts
+ *   moe_mx_quantize / moe_mx_dequantize / moe_mx_row_bytes
+ *                             bf16 rows to microscaled 8- or 4-bit rows and back
+ *   moe_expert_gate_up_mx / moe_expert_down_mx
+ *                             the experts' FFN on MX operands, over ragged blocks
  *   moe_dispatch_static       dispatch without a caller workspace
  *   moe_permute_bounded / moe_combine_bounded
  *                             permute / combine with dest_pos bounds-checked
@@ -446,6 +452,105 @@ moe_status moe_expert_gate_up(const moe_bf16_t *xs, const int32_t *offsets, cons
 moe_status moe_expert_down(const moe_bf16_t *h, const int32_t *offsets, const moe_bf16_t *w2,
                            const float *b2, int32_t E, int32_t d, int32_t F, int64_t rows,
                            moe_bf16_t *y, int32_t *d_status, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Microscaled (MX) rows: 8- and 4-bit operands.  The gpt-oss experts' weights
+ * come in this form, 4 bits a value ("I modelli MoE open hanno router
+ * opposti"); the pages give no layout, and the reading here is the public
+ * Microscaling formats specification: 32 values share a power-of-two scale.
+ *
+ * An MX row of K values (K a multiple of 8) is two byte rows:
+ *   elements  Kp = K rounded up to 128 values, zeros behind K.
+ *             MOE_MX_E4M3: one byte a value (8-bit float, largest 448);
+ *             MOE_MX_E2M1: two values a byte, the even column in the low half
+ *             (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives).
+ *   scales    Kp / 32 bytes, then zeros up to a multiple of 16 bytes.  Byte b
+ *             of block c stands for 2^(b - 127), b = 255 for "not a number".
+ *   value     = element * 2^(b - 127).
+ * moe_mx_row_bytes gives both lengths; rows follow one another without gaps.
+ * Element arrays are 32-byte aligned, scale arrays 16-byte aligned.  Both
+ * lengths are multiples of 16 bytes, so moe_permute moves MX rows (d = bytes / 2).
+ * ------------------------------------------------------------------------ */
+typedef enum { MOE_MX_E4M3 = 0, MOE_MX_E2M1 = 1 } moe_mx_format;
+
+/*
+ * moe_mx_row_bytes -- bytes of a row's elements and of its scales.
+ * 8 <= K <= 262144, K % 8 == 0.
+ */
+moe_status moe_mx_row_bytes(int32_t K, int32_t format, int64_t *row_bytes, int64_t *scale_bytes);
+
+/*
+ * moe_mx_quantize -- MX rows of bf16 rows.
+ *   scale of a block: the smallest power of two, 2^-127 at least, with which
+ *   none of its 32 values saturates; element = value / scale, rounded to
+ *   nearest, ties to even.
+ * Exact in every bit: neither the maximum nor the division by a power of two
+ * rounds.  A block that holds an infinity or NaN gets scale 255 and zero
+ * elements (it reads back as NaN).  A block of zeros gets scale byte 0.
+ * x [rows][K] bf16, 16-byte aligned.  The padding is written.
+ */
+moe_status moe_mx_quantize(const moe_bf16_t *x, int64_t rows, int32_t K, int32_t format, uint8_t *q,
+                           uint8_t *scales, moe_stream_t stream);
+
+/*
+ * moe_mx_dequantize -- out[r][c] = bf16(element * scale) of MX rows (exact but
+ * below bf16's normal range).  out [rows][K] bf16, 16-byte aligned.
+ */
+moe_status moe_mx_dequantize(const uint8_t *q, const uint8_t *scales, int64_t rows, int32_t K,
+                             int32_t format, moe_bf16_t *out, moe_stream_t stream);
+
+/*
+ * moe_add_rmsnorm -- the residual's addition and the norm in front of the
+ * router (the pages start at the normed hidden row; this is the step that
+ * makes it), with the experts' operand as a further output.
+ *   h  = bf16(x + residual)       (h = x if residual is NULL)
+ *   y  = bf16(h / sqrt(mean(h^2) + eps) * gain)
+ *   MX rows of y, bit for bit moe_mx_quantize's
+ * x, residual, residual_out, y [T][d] bf16; gain [d] bf16; q, scales MX rows of
+ * `format`.  residual_out (= h), y and q with scales are nullable, not all of
+ * them.  residual_out may be residual or x, y may be x or residual (not both
+ * outputs the same).  8 <= d <= 16384, d % 8 == 0, eps >= 0.  The mean is
+ * taken in fp32.  As the formula has it, a NaN makes its whole row of y NaN, an
+ * infinity gives NaN in its place and zeros beside it.
+ */
+moe_status moe_add_rmsnorm(const moe_bf16_t *x, const moe_bf16_t *residual, const moe_bf16_t *gain,
+                           float eps, int64_t T, int32_t d, moe_bf16_t *residual_out, moe_bf16_t *y,
+                           int32_t format, uint8_t *q, uint8_t *scales, moe_stream_t stream);
+
+/*
+ * moe_expert_gate_up_mx -- moe_expert_gate_up on MX operands:
+ *   h[r] = MX( act(xs[r] . W1[e]^T + b1[e], xs[r] . W3[e]^T + b3[e]) )
+ * with e the expert whose block [offsets[e], offsets[e+1]) holds row r.  The
+ * blocks are ragged: offsets as moe_dispatch writes them (or padded ones; the
+ * rows between are rows like any other).  No row outside the blocks is read
+ * into a result or written.
+ * xq, xs: MX rows of d values, `rows` of them; w1, w3 (and their scales): MX
+ * rows of d values, [E][F] of them; b1, b3 [E][F] fp32, 16-byte aligned, or
+ * NULL; h, h_scales: MX rows of F values, padding written.  Products are
+ * exact and accumulate in fp32 on tcgen05 tensor cores; bias and activation
+ * in fp32; one rounding, to h_format.  x_format, w_format, h_format: any.
+ * d, F multiples of 8; E <= 4096.  Offsets that descend, are negative or
+ * leave the rows report MOE_ERR_DEVICE_INDEX, and nothing is written.
+ */
+moe_status moe_expert_gate_up_mx(const uint8_t *xq, const uint8_t *xs, int32_t x_format,
+                                 const int32_t *offsets, const uint8_t *w1,
+                                 const uint8_t *w1_scales, const uint8_t *w3,
+                                 const uint8_t *w3_scales, int32_t w_format, const float *b1,
+                                 const float *b3, int32_t E, int32_t d, int32_t F, int64_t rows,
+                                 int32_t act, uint8_t *h, uint8_t *h_scales, int32_t h_format,
+                                 int32_t *d_status, moe_stream_t stream);
+
+/*
+ * moe_expert_down_mx -- y[r] = bf16( h[r] . W2[e]^T + b2[e] )
+ * h, h_scales: MX rows of F values; w2, w2_scales: MX rows of F values, [E][d]
+ * of them; b2 [E][d] fp32, 16-byte aligned, or NULL; y [rows][d] bf16 (the
+ * expert outputs moe_combine reads).  Blocks, limits and status as
+ * moe_expert_gate_up_mx.
+ */
+moe_status moe_expert_down_mx(const uint8_t *h, const uint8_t *h_scales, int32_t h_format,
+                              const int32_t *offsets, const uint8_t *w2, const uint8_t *w2_scales,
+                              int32_t w_format, const float *b2, int32_t E, int32_t d, int32_t F,
+                              int64_t rows, moe_bf16_t *y, int32_t *d_status, moe_stream_t stream);
 
 #ifdef __cplusplus
 }

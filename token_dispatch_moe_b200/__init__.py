@@ -14,6 +14,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -25,6 +26,8 @@ __all__ = [
     "moe_status_string", "moe_gate_gemm", "moe_gate_route", "moe_route", "moe_hash_route",
     "moe_dispatch_workspace_size", "moe_dispatch", "moe_dispatch_static", "moe_permute",
     "moe_combine", "moe_permute_bounded", "moe_combine_bounded",
+    "MOE_MX_E4M3", "MOE_MX_E2M1", "MxRows", "moe_mx_row_bytes", "moe_mx_quantize",
+    "moe_mx_dequantize", "moe_add_rmsnorm", "moe_expert_gate_up_mx", "moe_expert_down_mx",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -103,6 +106,13 @@ def load_library(path: str | None = None, strict: bool = True):
         "moe_combine": ([P, P, P, P, i64, i32, i32, P, P], st),
         "moe_permute_bounded": ([P, P, i64, i32, i32, P, i64, P, P], st),
         "moe_combine_bounded": ([P, P, P, P, i64, i32, i32, i64, P, P, P], st),
+        "moe_mx_row_bytes": ([i32, i32, ctypes.POINTER(i64), ctypes.POINTER(i64)], st),
+        "moe_mx_quantize": ([P, i64, i32, i32, P, P, P], st),
+        "moe_mx_dequantize": ([P, P, i64, i32, i32, P, P], st),
+        "moe_add_rmsnorm": ([P, P, P, ctypes.c_float, i64, i32, P, P, i32, P, P, P], st),
+        "moe_expert_gate_up_mx": ([P, P, i32, P, P, P, P, P, i32, P, P, i32, i32, i32, i64, i32,
+                                   P, P, i32, P, P], st),
+        "moe_expert_down_mx": ([P, P, i32, P, P, P, i32, P, i32, i32, i32, i64, P, P, P], st),
     }
     for name, (args, res) in sig.items():
         if not strict and not hasattr(lib, name):
@@ -404,6 +414,133 @@ def moe_expert_down(h, offsets, w2, y, b2=None, d_status=None, stream=None):
     _check(load_library().moe_expert_down(_ptr(h), _ptr(offsets), _ptr(w2), _ptr(b2), E, d, F,
                                           rows, _ptr(y), _ptr(d_status), _stream(stream)),
            "moe_expert_down")
+
+
+MOE_MX_E4M3, MOE_MX_E2M1 = 0, 1
+
+
+class MxRows(NamedTuple):
+    """Microscaled rows (layout: the C header): ``q`` uint8 [..., row bytes],
+    ``scales`` uint8 [..., scale bytes], the ``K`` values a row stands for and
+    its ``format`` (MOE_MX_E4M3 or MOE_MX_E2M1).  The leading sizes are the
+    rows' ([T], or [E, F] for the experts' weights)."""
+    q: torch.Tensor
+    scales: torch.Tensor
+    K: int
+    format: int
+
+    @classmethod
+    def empty(cls, lead, K: int, format: int, device="cuda") -> "MxRows":
+        """Uninitialised rows; ``lead``: their leading sizes."""
+        row, scale = moe_mx_row_bytes(K, format)
+        return cls(torch.empty((*lead, row), dtype=torch.uint8, device=device),
+                   torch.empty((*lead, scale), dtype=torch.uint8, device=device), K, format)
+
+    def as_bf16_rows(self):
+        """(elements, scales) of [T] rows viewed as bf16 tensors, as moe_permute takes rows to
+        move them: permute both with one dest_pos."""
+        return self.q.view(torch.bfloat16), self.scales.view(torch.bfloat16)
+
+
+def moe_mx_row_bytes(K: int, format: int) -> tuple[int, int]:
+    """Bytes of a row's elements and of its scales."""
+    row, scale = ctypes.c_int64(0), ctypes.c_int64(0)
+    _check(load_library().moe_mx_row_bytes(K, format, ctypes.byref(row), ctypes.byref(scale)),
+           "moe_mx_row_bytes")
+    return row.value, scale.value
+
+
+def _need_mx(mx, name, ndim=2):
+    """Checks MX rows' tensors; the leading sizes are returned."""
+    q, scales, K, fmt = mx
+    _need(q, torch.uint8, name, ndim)
+    _need(scales, torch.uint8, f"{name} scales", ndim)
+    if K < 8 or K % 8 or fmt not in (MOE_MX_E4M3, MOE_MX_E2M1):
+        raise ValueError(f"{name}: K must be a multiple of 8 and the format E4M3 or E2M1")
+    padded = (K + 127) // 128 * 128
+    if q.shape[-1] != (padded if fmt == MOE_MX_E4M3 else padded // 2) or \
+            scales.shape[-1] != (padded // 32 + 15) // 16 * 16 or q.shape[:-1] != scales.shape[:-1]:
+        raise ValueError(f"{name}: shape mismatch")
+    return q.shape[:-1]
+
+
+def moe_mx_quantize(x, out: MxRows, stream=None):
+    """out = MX rows of the bf16 rows x [..., K]."""
+    lead = _need_mx(out, "out", x.dim())
+    _need(x, torch.bfloat16, "x")
+    if x.shape != (*lead, out.K):
+        raise ValueError("shape mismatch")
+    _check(load_library().moe_mx_quantize(_ptr(x), math.prod(lead), out.K, out.format, _ptr(out.q),
+                                          _ptr(out.scales), _stream(stream)), "moe_mx_quantize")
+
+
+def moe_mx_dequantize(mx: MxRows, out, stream=None):
+    """out [..., K] bf16 = the values of MX rows."""
+    lead = _need_mx(mx, "mx", out.dim())
+    _need(out, torch.bfloat16, "out")
+    if out.shape != (*lead, mx.K):
+        raise ValueError("shape mismatch")
+    _check(load_library().moe_mx_dequantize(_ptr(mx.q), _ptr(mx.scales), math.prod(lead), mx.K,
+                                            mx.format, _ptr(out), _stream(stream)),
+           "moe_mx_dequantize")
+
+
+def moe_add_rmsnorm(x, residual, gain, eps, residual_out=None, y=None, mx: MxRows | None = None,
+                    stream=None):
+    """h = bf16(x + residual) (h = x without one) to residual_out, y = the RMS norm of h times
+    gain, mx = y's MX rows; outputs that are None are not written."""
+    _need(x, torch.bfloat16, "x", 2)
+    _need(gain, torch.bfloat16, "gain", 1)
+    for t, n in ((residual, "residual"), (residual_out, "residual_out"), (y, "y")):
+        _need(t, torch.bfloat16, n)
+        if t is not None and t.shape != x.shape:
+            raise ValueError("shape mismatch")
+    T, d = x.shape
+    if gain.shape[0] != d or (mx is not None and (_need_mx(mx, "mx") != (T,) or mx.K != d)):
+        raise ValueError("shape mismatch")
+    q, scales, _, fmt = mx if mx is not None else (None, None, d, 0)
+    _check(load_library().moe_add_rmsnorm(_ptr(x), _ptr(residual), _ptr(gain), eps, T, d,
+                                          _ptr(residual_out), _ptr(y), fmt, _ptr(q), _ptr(scales),
+                                          _stream(stream)), "moe_add_rmsnorm")
+
+
+def moe_expert_gate_up_mx(xs: MxRows, offsets, w1: MxRows, w3: MxRows, h: MxRows, b1=None, b3=None,
+                          act=MOE_ACT_SWIGLU, d_status=None, stream=None):
+    """h = MX(act(xs W1[e]^T + b1[e], xs W3[e]^T + b3[e])) over the ragged expert blocks of
+    offsets (w1, w3: [E, F] rows of d values; xs: [rows] of d values; h: [rows] of F values)."""
+    _need(offsets, torch.int32, "offsets", 1)
+    (rows,) = _need_mx(xs, "xs")
+    E, F = _need_mx(w1, "w1", 3)
+    for b, n in ((b1, "b1"), (b3, "b3")):
+        _need(b, torch.float32, n, 2)
+        if b is not None and b.shape != (E, F):
+            raise ValueError("shape mismatch")
+    _need(d_status, torch.int32, "d_status")
+    if _need_mx(w3, "w3", 3) != (E, F) or _need_mx(h, "h") != (rows,) or w1.K != xs.K or \
+            w3.K != xs.K or w3.format != w1.format or h.K != F or offsets.shape[0] != E + 1:
+        raise ValueError("shape mismatch")
+    _check(load_library().moe_expert_gate_up_mx(
+        _ptr(xs.q), _ptr(xs.scales), xs.format, _ptr(offsets), _ptr(w1.q), _ptr(w1.scales),
+        _ptr(w3.q), _ptr(w3.scales), w1.format, _ptr(b1), _ptr(b3), E, xs.K, F, rows, act,
+        _ptr(h.q), _ptr(h.scales), h.format, _ptr(d_status), _stream(stream)),
+        "moe_expert_gate_up_mx")
+
+
+def moe_expert_down_mx(h: MxRows, offsets, w2: MxRows, y, b2=None, d_status=None, stream=None):
+    """y = bf16(h W2[e]^T + b2[e]) over the ragged expert blocks of offsets (w2: [E, d] rows of
+    F values; h: [rows] of F values; y: [rows, d])."""
+    _need(offsets, torch.int32, "offsets", 1)
+    _need(y, torch.bfloat16, "y", 2)
+    _need(b2, torch.float32, "b2", 2)
+    _need(d_status, torch.int32, "d_status")
+    (rows,) = _need_mx(h, "h")
+    E, d = _need_mx(w2, "w2", 3)
+    if w2.K != h.K or y.shape != (rows, d) or offsets.shape[0] != E + 1 or \
+            (b2 is not None and b2.shape != (E, d)):
+        raise ValueError("shape mismatch")
+    _check(load_library().moe_expert_down_mx(
+        _ptr(h.q), _ptr(h.scales), h.format, _ptr(offsets), _ptr(w2.q), _ptr(w2.scales), w2.format,
+        _ptr(b2), E, d, h.K, rows, _ptr(y), _ptr(d_status), _stream(stream)), "moe_expert_down_mx")
 
 
 def moe_wait_probe(limit_ns: int, d_status, d_outcome=None, stream=None):

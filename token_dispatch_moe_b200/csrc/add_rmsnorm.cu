@@ -1,0 +1,171 @@
+// moe_add_rmsnorm: the residual's addition and the root-mean-square norm in
+// front of the router, with the experts' MX rows as a further output.
+//
+//   h = bf16(x + residual)                         (h = x without a residual)
+//   y = bf16(h * (mean(h^2) + eps)^(-1/2) * gain)
+//   mx = MX rows of y
+//
+// h is rounded before the norm: it is what the next layer reads, so the norm
+// is the norm of the stored stream and does not depend on whether the addition
+// was fused.  The MX rows are made of the rounded y: the gate and the experts
+// see one and the same row, and the bits are moe_mx_quantize's on y.
+//
+// One pass, bound by memory (9.03 bytes a value with every output): a block of
+// threads owns a row and keeps it in registers between the sum of squares and
+// the outputs.  The sum is fp32: at most 8 vectors of 8 values in a thread, then a
+// tree over the block.
+#include "mx.cuh"
+#include "rows.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kNormMaxD = 16384;
+
+struct NormArgs {
+    const moe_bf16_t *x, *residual, *gain;
+    moe_bf16_t *residual_out, *y;
+    uint8_t *q, *scales;
+    int64_t row_bytes, scale_bytes;
+    int32_t data, padded;  // 8-value vectors of a row, without and with its padding
+    float eps, inv_d;
+};
+
+// FMT -1: no MX output.  VPT vectors a thread: vector v = u * blockDim.x + threadIdx.x.
+template <int VPT, int FMT>
+__global__ void __launch_bounds__(256) add_rmsnorm_kernel(const NormArgs a) {
+    __shared__ float part[8];
+    griddep_wait();
+    const int64_t row = blockIdx.x;
+    const uint4 *x = reinterpret_cast<const uint4 *>(a.x) + row * a.data;
+    const uint4 *r = reinterpret_cast<const uint4 *>(a.residual) + row * a.data;
+    uint4 h[VPT], g[VPT];
+    {
+        uint4 rin[VPT];
+#pragma unroll
+        for (int u = 0; u < VPT; ++u) {
+            const int v = u * blockDim.x + threadIdx.x;
+            h[u] = rin[u] = make_uint4(0u, 0u, 0u, 0u);
+            if (v < a.data) {
+                h[u] = ld_stream(x + v);
+                if (a.residual) rin[u] = ld_stream(r + v);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < VPT; ++u) {
+            const int v = u * blockDim.x + threadIdx.x;
+            g[u] = make_uint4(0u, 0u, 0u, 0u);
+            if (v < a.data) g[u] = *(reinterpret_cast<const uint4 *>(a.gain) + v);
+        }
+        if (a.residual) {
+#pragma unroll
+            for (int u = 0; u < VPT; ++u) {
+                float f[8];
+                unpack_bf16x8(h[u], f);
+                add_bf16x8(f, rin[u]);
+                h[u] = pack_bf16x8(f);
+            }
+        }
+    }
+    griddep_launch_dependents();
+    float sum = 0.0f;
+#pragma unroll
+    for (int u = 0; u < VPT; ++u) {
+        float f[8];
+        unpack_bf16x8(h[u], f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum = fmaf(f[i], f[i], sum);
+    }
+    sum = warp_sum(sum);
+    const int warps = blockDim.x >> 5;
+    if (warps > 1) {
+        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sum;
+        __syncthreads();
+        sum = 0.0f;
+        for (int w = 0; w < warps; ++w) sum += part[w];
+    }
+    const float inv = rsqrtf(fmaf(sum, a.inv_d, a.eps));
+#pragma unroll
+    for (int u = 0; u < VPT; ++u) {
+        const int v = u * blockDim.x + threadIdx.x;
+        float f[8], gf[8];
+        unpack_bf16x8(h[u], f);
+        unpack_bf16x8(g[u], gf);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = f[i] * inv * gf[i];
+        uint4 y = pack_bf16x8(f);
+        if (v >= a.data) y = make_uint4(0u, 0u, 0u, 0u);  // 0 * a NaN row's factor is not 0
+        if (v < a.data) {
+            if (a.residual_out) reinterpret_cast<uint4 *>(a.residual_out)[row * a.data + v] = h[u];
+            if (a.y) reinterpret_cast<uint4 *>(a.y)[row * a.data + v] = y;
+        }
+        if (FMT >= 0) {
+            constexpr int F = FMT < 0 ? 0 : FMT;
+            unpack_bf16x8(y, f);
+            uint32_t byte;
+            const uint2 e = mx_quarter<F>(f, byte);
+            uint8_t *srow = a.scales + row * a.scale_bytes;
+            if (v < a.padded) mx_store<F>(a.q + row * a.row_bytes, srow, v, e, byte);
+            if (v + 1 == a.padded)
+                for (int64_t b = a.padded / 4; b < a.scale_bytes; ++b) srow[b] = 0;
+        }
+    }
+}
+
+template <int FMT>
+cudaError_t launch_norm(const NormArgs &a, int64_t T, cudaStream_t s) {
+    // The fewest vectors a thread with which a row fits 256 threads.
+    const int vecs = FMT >= 0 ? a.padded : a.data;
+    int vpt = 1;
+    while (vpt * 256 < vecs) vpt *= 2;
+    const dim3 grid((unsigned)T), block((unsigned)(((vecs + vpt - 1) / vpt + 31) / 32 * 32));
+    switch (vpt) {
+        case 1: return launch_pdl(add_rmsnorm_kernel<1, FMT>, grid, block, 0, s, a);
+        case 2: return launch_pdl(add_rmsnorm_kernel<2, FMT>, grid, block, 0, s, a);
+        case 4: return launch_pdl(add_rmsnorm_kernel<4, FMT>, grid, block, 0, s, a);
+        default: return launch_pdl(add_rmsnorm_kernel<8, FMT>, grid, block, 0, s, a);
+    }
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" moe_status moe_add_rmsnorm(const moe_bf16_t *x, const moe_bf16_t *residual,
+                                      const moe_bf16_t *gain, float eps, int64_t T, int32_t d,
+                                      moe_bf16_t *residual_out, moe_bf16_t *y, int32_t format,
+                                      uint8_t *q, uint8_t *scales, moe_stream_t stream) {
+    using namespace moe;
+    if (T < 0 || d < 8 || d % 8 != 0 || !(eps >= 0.0f)) return MOE_ERR_INVALID_ARG;
+    if (q && (!mx_format_ok(format) || !scales)) return MOE_ERR_INVALID_ARG;
+    if (!q && scales) return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    if (!x || !gain || (!residual_out && !y && !q)) return MOE_ERR_INVALID_ARG;
+    for (const void *p : {(const void *)x, (const void *)residual, (const void *)gain,
+                          (const void *)residual_out, (const void *)y})
+        if (!aligned16(p)) return MOE_ERR_INVALID_ARG;
+    if (!mx_aligned(q, scales)) return MOE_ERR_INVALID_ARG;
+    if (d > kNormMaxD || T >= (int64_t)INT32_MAX) return MOE_ERR_UNSUPPORTED;
+    NormArgs a;
+    a.x = x;
+    a.residual = residual;
+    a.gain = gain;
+    a.residual_out = residual_out;
+    a.y = y;
+    a.q = q;
+    a.scales = scales;
+    a.row_bytes = q ? mx_row_bytes(d, format) : 0;
+    a.scale_bytes = q ? mx_scale_bytes(d) : 0;
+    a.data = d / 8;
+    a.padded = mx_padded(d) / 8;
+    a.eps = eps;
+    a.inv_d = 1.0f / (float)d;
+    const cudaStream_t s = as_cuda(stream);
+    const cudaError_t e = !q                        ? launch_norm<-1>(a, T, s)
+                          : format == MOE_MX_E4M3 ? launch_norm<MOE_MX_E4M3>(a, T, s)
+                                                  : launch_norm<MOE_MX_E2M1>(a, T, s);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return MOE_ERR_CUDA;
+    }
+    return launch_status();
+}

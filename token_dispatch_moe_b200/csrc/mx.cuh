@@ -1,0 +1,127 @@
+// Microscaled (MX) rows, shared by the kernels that write or read them.
+//
+// A row of K values is cut into blocks of 32; a block holds 32 small floats
+// (e4m3: 4 exponent and 3 mantissa bits, largest 448; e2m1: 2 and 1, largest
+// 6) and one scale byte b that stands for 2^(b - 127) (255: not a number).
+// value = element * 2^(b - 127).  Internal to libmoe_dispatch.
+#pragma once
+
+#include "common.cuh"
+
+namespace moe {
+
+constexpr int kMxBlock = 32;        // values that share a scale
+constexpr int kMxPad = 128;         // rows are zero-padded to this many values
+constexpr int kMxMaxK = 1 << 18;    // widest row
+
+inline bool mx_format_ok(int32_t f) { return f == MOE_MX_E4M3 || f == MOE_MX_E2M1; }
+inline int32_t mx_padded(int32_t K) { return (K + kMxPad - 1) / kMxPad * kMxPad; }
+inline int64_t mx_row_bytes(int32_t K, int32_t format) {
+    return format == MOE_MX_E4M3 ? mx_padded(K) : mx_padded(K) / 2;
+}
+// 16-byte multiples: a row's scales can be moved by the row movers and by TMA.
+inline int64_t mx_scale_bytes(int32_t K) { return (mx_padded(K) / kMxBlock + 15) / 16 * 16; }
+inline bool mx_aligned(const void *q, const void *scales) {
+    // 32 bytes: what the copy that widens packed 4-bit values asks of a matrix
+    return (reinterpret_cast<uintptr_t>(q) & 31u) == 0 && aligned16(scales);
+}
+
+// Scale byte of a block from the bits of its largest magnitude (the unsigned
+// maximum of the values' bits without their sign, so infinities and NaN win):
+// the smallest power of two with which nothing saturates.  With the largest
+// magnitude 1.m * 2^(E-127) and the format's largest value 1.75 * 2^8 or
+// 1.5 * 2^2, that is 2^(E-127-8) (or -2), doubled if 1.m exceeds 1.75 (1.5).
+// Rounding the power up, where the MX paper's rule rounds it down, keeps the
+// block's largest value (up to a quarter of it would be cut off with e2m1).
+template <int FMT>
+__device__ __forceinline__ uint32_t mx_scale_byte(uint32_t amax_bits) {
+    constexpr int emax = FMT == MOE_MX_E4M3 ? 8 : 2;
+    constexpr uint32_t top = FMT == MOE_MX_E4M3 ? 0x600000u : 0x400000u;
+    const int e = (int)(amax_bits >> 23);
+    if (e == 255) return 255u;
+    const int b = e - emax + ((amax_bits & 0x7fffffu) > top ? 1 : 0);
+    return (uint32_t)(b > 0 ? b : 0);
+}
+
+// 2^(127 - b): the exact factor from a value to its element (b <= 253 here).
+__device__ __forceinline__ float mx_inverse(uint32_t b) {
+    return __uint_as_float((254u - b) << 23);
+}
+
+// 2^(b - 127): 2^-127 is the one subnormal, 255 is NaN.
+__device__ __forceinline__ float mx_scale(uint32_t b) {
+    return __uint_as_float(b == 0 ? 0x00400000u : b == 255u ? 0x7fc00000u : b << 23);
+}
+
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// Eight scaled values to elements, nearest with ties to even: 8 bytes (e4m3)
+// or 4 bytes in .x (e2m1, even columns in the low halves).
+template <int FMT>
+__device__ __forceinline__ uint2 mx_pack8(const float (&v)[8]) {
+    if (FMT == MOE_MX_E4M3) {
+        uint32_t r[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            asm("{\n\t.reg .b16 lo, hi;\n\t"
+                "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+                "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+                "mov.b32 %0, {lo, hi};\n\t}"
+                : "=r"(r[i])
+                : "f"(v[4 * i]), "f"(v[4 * i + 1]), "f"(v[4 * i + 2]), "f"(v[4 * i + 3]));
+        return make_uint2(r[0], r[1]);
+    }
+    uint32_t r;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+        : "=r"(r)
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    return make_uint2(r, 0u);
+}
+
+// A quarter block (8 values) of a lane whose neighbours in its group of four
+// hold the rest of the block: the block's scale byte and this lane's elements.
+// A block that holds an infinity or NaN gets scale 255 and zero elements: it
+// reads back as NaN, so nothing that is not a number passes for one.
+template <int FMT>
+__device__ __forceinline__ uint2 mx_quarter(const float (&v)[8], uint32_t &byte) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i]));
+    m = max(m, __shfl_xor_sync(MOE_FULL_MASK, m, 1));
+    m = max(m, __shfl_xor_sync(MOE_FULL_MASK, m, 2));
+    byte = mx_scale_byte<FMT>(m);
+    const float inv = mx_inverse(byte);
+    float s[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] = v[i] * inv;
+    const uint2 q = mx_pack8<FMT>(s);
+    return byte == 255u ? make_uint2(0u, 0u) : q;
+}
+
+// The lane's elements at vector `vec` (8 values) of a row, and by the first
+// lane of each four the block's scale.
+template <int FMT>
+__device__ __forceinline__ void mx_store(uint8_t *row, uint8_t *scales, int vec, uint2 q,
+                                         uint32_t byte) {
+    if (FMT == MOE_MX_E4M3)
+        *reinterpret_cast<uint2 *>(row + 8 * (int64_t)vec) = q;
+    else
+        *reinterpret_cast<uint32_t *>(row + 4 * (int64_t)vec) = q.x;
+    if ((vec & 3) == 0) scales[vec >> 2] = (uint8_t)byte;
+}
+
+__device__ __forceinline__ void unpack_bf16x8(const uint4 &v, float (&f)[8]) {
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(u[i] << 16);
+        f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+}
+
+}  // namespace moe

@@ -206,6 +206,70 @@ __device__ __forceinline__ void umma_commit_pair(uint32_t bar) {
         : "memory");
 }
 
+// ------------------------------------------------- block-scaled MMA (MX rows)
+// D[128][N] += (A . scaleA) (B . scaleB)^T over 32 K values: every row of A and
+// of B has one power-of-two scale byte for these 32 values.  Elements are 8-bit
+// containers in shared memory (K-major, 128-byte swizzle): e4m3, or e2m1 with a
+// 16-byte group of 16 values holding 8 packed bytes, as the widening TMA load
+// writes it.  Scales lie in TMEM: row r's byte for K step j of a group of four
+// is byte j of the word at lane r % 32 (repeated in the four lane quarters),
+// column base + r / 32.
+
+// Instruction descriptor of the block-scaled MMA, without the scale byte ids:
+// A type [7,10), B type [10,13) (0 e4m3, 5 e2m1), N / 8 at 17, power-of-two
+// scales (bit 23), M / 128 at 27.
+__host__ __device__ __forceinline__ uint32_t mx_idesc(uint32_t a_type, uint32_t b_type,
+                                                      uint32_t m) {
+    return (a_type << 7) | (b_type << 10) | (1u << 23) | ((m >> 7) << 27);
+}
+// ... with N and the K step's scale byte (A: bits [29,31), B: [4,6)).
+__device__ __forceinline__ uint32_t mx_idesc_at(uint32_t idesc, uint32_t n, uint32_t k) {
+    return idesc | ((n >> 3) << 17) | (k << 29) | (k << 4);
+}
+
+__device__ __forceinline__ void umma_mx(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
+                                        uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                        uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X"
+        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(tmem_d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+// 512 bytes of scales (32 rows of 16 bytes, laid end to end) to four TMEM
+// columns, repeated in the four lane quarters.
+__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint32_t saddr) {
+    uint64_t d = 0;  // no swizzle: 8 rows of 16 bytes are 128 contiguous bytes
+    d |= (uint64_t)((saddr >> 4) & 0x3fffu);
+    d |= (uint64_t)(128u >> 4) << 16;
+    d |= (uint64_t)(128u >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d)
+                 : "memory");
+}
+
+// Generic-proxy shared-memory accesses before, async-proxy accesses after.
+__device__ __forceinline__ void fence_async_shared() {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
 // ----------------------------------------------------------- host side ----
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
                                   const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
@@ -237,6 +301,40 @@ inline bool make_map(CUtensorMap *m, const void *ptr, int64_t rows, int64_t cols
     cuuint32_t estr[2] = {1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(ptr), dims, strides, box,
                estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// 2-D tensor of bytes [rows][pitch], box = box_rows x box_bytes, no swizzle or (box of 128
+// bytes) the 128-byte one.
+inline bool make_byte_map(CUtensorMap *m, const void *ptr, int64_t rows, int64_t pitch,
+                          int box_rows, int box_bytes) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)pitch, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)pitch};
+    cuuint32_t box[2] = {(cuuint32_t)box_bytes, (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(ptr), dims, strides, box,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// 2-D tensor of packed 4-bit values [rows][cols] (cols a multiple of 128, 32-byte aligned),
+// box = box_rows x 128 values, widened to 8-bit containers in shared memory (16 values: 8
+// packed bytes and 8 unused), 128-byte swizzle.
+inline bool make_nibble_map(CUtensorMap *m, const void *ptr, int64_t rows, int64_t cols,
+                            int box_rows) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)cols / 2};
+    cuuint32_t box[2] = {128u, (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 2, const_cast<void *>(ptr), dims, strides,
+               box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
