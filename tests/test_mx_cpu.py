@@ -80,7 +80,6 @@ def test_expert_refusals(lib):
         assert down(lib, **kw) == BAD, kw
     for f in (gate_up, down):
         assert f(lib, rows=(1 << 31) - 1) == BIG
-        assert f(lib, E=4096, d=262144, F=262144) == BIG
         assert f(lib, d=262152) == BIG
 
 

@@ -21,7 +21,7 @@
 //   warps 2, 3 turn raw scale rows [row][16 bytes] into the tiles that TMEM
 //              wants (32 x 16 bytes, four rows' words side by side)
 //   warp 1     one thread: scale tiles to TMEM (tcgen05.cp), four MMAs a stage
-//   warps 4-7  epilogue: TMEM -> shared memory, transposed to token-major; each
+//   warps 4-11 epilogue: TMEM -> shared memory, transposed to token-major; each
 //              thread then takes 8 features of a token: bias, activation, MX
 //              block (four lanes) or bf16, and one vector store
 // Two accumulators: the epilogue of a tile overlaps the next one's products.
@@ -29,16 +29,17 @@
 // its 128 rows; they meet in the epilogue's shared memory.
 // Every wait is bounded, as in the bf16 kernels.
 #include "mx.cuh"
+#include "rows.cuh"
 #include "tc.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kXThreads = 256;
+constexpr int kXThreads = 384;
 constexpr int kXBK = 128;           // K values of a stage
 constexpr int kXSuper = 4;          // stages that one load of scales covers
 constexpr int kXMaxE = 4096;
-constexpr int kXEpiThreads = 128;
+constexpr int kXEpiThreads = 256;
 constexpr int kXChunk = 32;         // token columns the epilogue turns at a time
 constexpr int kXPitch = 132;        // floats of a staged token: 16-byte aligned, off the banks
 constexpr float kXOaiAlpha = 1.702f;
@@ -61,38 +62,119 @@ struct MxFfnArgs {
 
 // As in the bf16 kernel's epilogue: fast exponential and quotient, about 1e-6
 // relative, far below the rounding to 8 bits.
-__device__ __forceinline__ float activate(float g, float u, int act) {
+__device__ __forceinline__ void activate8(float (&g)[8], const float (&u)[8], int act) {
     if (act == MOE_ACT_SWIGLU_OAI) {
-        const float gc = fminf(g, kXOaiLimit);
-        const float uc = fminf(fmaxf(u, -kXOaiLimit), kXOaiLimit);
-        return __fdividef(gc, 1.0f + __expf(-kXOaiAlpha * gc)) * (uc + 1.0f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float gc = fminf(g[k], kXOaiLimit);
+            const float uc = fminf(fmaxf(u[k], -kXOaiLimit), kXOaiLimit);
+            g[k] = __fdividef(gc, 1.0f + __expf(-kXOaiAlpha * gc)) * (uc + 1.0f);
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) g[k] = __fdividef(g[k], 1.0f + __expf(-g[k])) * u[k];
     }
-    return __fdividef(g, 1.0f + __expf(-g)) * u;
+}
+
+__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
+    const float4 x = *reinterpret_cast<const float4 *>(p);
+    const float4 y = *reinterpret_cast<const float4 *>(p + 4);
+    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+    v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+}
+
+// 8 features of a row of h (four neighbouring lanes hold a block).
+__device__ __forceinline__ void store_h(const MxFfnArgs &a, int64_t row, int f, const float (&o)[8],
+                                        bool there) {
+    uint8_t *qrow = a.hq + row * a.h_row, *srow = a.hs + row * a.h_scale;
+    uint32_t byte;
+    if (a.h_fmt == MOE_MX_E4M3) {
+        const uint2 e = mx_quarter<MOE_MX_E4M3>(o, byte);
+        if (there) mx_store<MOE_MX_E4M3>(qrow, srow, f >> 3, e, byte);
+    } else {
+        const uint2 e = mx_quarter<MOE_MX_E2M1>(o, byte);
+        if (there) mx_store<MOE_MX_E2M1>(qrow, srow, f >> 3, e, byte);
+    }
+}
+
+// Raw scale rows (16 bytes: four stages' words) to the four stages' tiles, `step` bytes apart:
+// every second of `pieces` 32-row pieces, rows below `rows`.
+__device__ __forceinline__ void turn_scales(const uint8_t *raw, uint8_t *tiles, int step, int first,
+                                            int pieces, int rows, int row0, int dst0) {
+    for (int i = first; i < pieces; i += 2) {
+        const int r = (i >> 2) * 128 + 8 * (i & 3) + row0;
+        if (r >= rows) continue;
+        const uint4 v = *reinterpret_cast<const uint4 *>(raw + r * 16);
+        uint8_t *dst = tiles + (i >> 2) * 512 + (i & 3) * 128 + dst0;
+        *reinterpret_cast<uint32_t *>(dst) = v.x;
+        *reinterpret_cast<uint32_t *>(dst + step) = v.y;
+        *reinterpret_cast<uint32_t *>(dst + 2 * step) = v.z;
+        *reinterpret_cast<uint32_t *>(dst + 3 * step) = v.w;
+    }
 }
 
 struct Tile {
     int e, row0, n, f0;
 };
 
-// Tile t of the walk: its expert by bisection of the part counts before each
-// expert, its share of the block's rows (a multiple of 8 but for the last).
-__device__ __forceinline__ Tile tile_at(const MxFfnArgs &a, const int32_t *off,
-                                        const int32_t *parts, int64_t t) {
-    const int p = (int)(t / a.f_tiles);
-    int lo = 0, hi = a.E - 1;
-    while (lo < hi) {  // the last e with parts[e] <= p
-        const int mid = (lo + hi + 1) >> 1;
-        if (parts[mid] <= p) lo = mid; else hi = mid - 1;
+// The tiles of one CTA in order: tile t = part * f_tiles + feature tile, t = blockIdx.x,
+// + gridDim.x, ...  Every role of the CTA walks them.  The quotients are carried along:
+// a runtime division in a role's loop costs as much as issuing a stage.
+struct Walk {
+    const int32_t *off, *parts;
+    int E, ft, f_tiles, step_p, step_f;
+    int p, f, e;
+
+    __device__ __forceinline__ Walk(const MxFfnArgs &a, const int32_t *o, const int32_t *q)
+        : off(o), parts(q), E(a.E), ft(a.ft), f_tiles(a.f_tiles) {
+        step_p = (int)gridDim.x / f_tiles;
+        step_f = (int)gridDim.x - step_p * f_tiles;
+        p = (int)blockIdx.x / f_tiles;
+        f = (int)blockIdx.x - p * f_tiles;
+        e = 0;
     }
-    const int m = off[lo + 1] - off[lo], of = parts[lo + 1] - parts[lo];
-    const int share = ((m + of - 1) / of + 7) & ~7;  // <= cap, so no part is empty
-    Tile w;
-    w.e = lo;
-    w.row0 = off[lo] + (p - parts[lo]) * share;
-    w.n = min(share, off[lo + 1] - w.row0);
-    w.f0 = (int)(t - (int64_t)p * a.f_tiles) * a.ft;
-    return w;
-}
+    __device__ __forceinline__ void next() {
+        p += step_p;
+        f += step_f;
+        if (f >= f_tiles) {
+            f -= f_tiles;
+            ++p;
+        }
+    }
+    // False behind the last tile.  The expert by bisection of the part counts before each
+    // expert, its share of the block's rows a multiple of 8 but for the last part's.
+    __device__ __forceinline__ bool tile(Tile &w) {
+        if (p >= parts[E]) return false;
+        if (parts[e + 1] <= p) {
+            int lo = e + 1, hi = E - 1;
+            while (lo < hi) {  // the last e with parts[e] <= p
+                const int mid = (lo + hi + 1) >> 1;
+                if (parts[mid] <= p) lo = mid; else hi = mid - 1;
+            }
+            e = lo;
+        }
+        const int first = off[e], m = off[e + 1] - first;
+        const int of = parts[e + 1] - parts[e];
+        const int share = of == 1 ? m : ((m + of - 1) / of + 7) & ~7;  // <= cap: no part is empty
+        w.e = e;
+        w.row0 = first + (p - parts[e]) * share;
+        w.n = min(share, first + m - w.row0);
+        w.f0 = f * ft;
+        return true;
+    }
+};
+
+// A place in a ring of `size` buffers and the parity of the pass over it.
+struct Ring {
+    int at = 0;
+    uint32_t pass = 0;
+    __device__ __forceinline__ void next(int size) {
+        if (++at == size) {
+            at = 0;
+            pass ^= 1u;
+        }
+    }
+};
 
 __device__ __forceinline__ void epi_sync() {
     asm volatile("bar.sync 1, %0;" ::"n"(kXEpiThreads) : "memory");
@@ -139,7 +221,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(tfull_bar(b), 1);
-            mbar_init(tempty_bar(b), 4);  // one arrival per epilogue warp
+            mbar_init(tempty_bar(b), 8);  // one arrival per epilogue warp
         }
         mbar_init(drain_bar, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -176,161 +258,171 @@ __global__ void __launch_bounds__(kXThreads, 1)
         }
         if (lane == 0) parts[0] = 0;
     }
+    if (any_bad && threadIdx.x == 0) parts[a.E] = 0;  // no tiles
     __syncthreads();
     if (any_bad && threadIdx.x == 0 && blockIdx.x == 0) report(a.status, MOE_ERR_DEVICE_INDEX);
-    const int64_t num_tiles = any_bad ? 0 : (int64_t)parts[a.E] * a.f_tiles;
     volatile int *abort_v = &abort_s;
     griddep_launch_dependents();
 
-    if (warp == 0 && lane == 0) {
-        uint32_t it = 0, sit = 0;
-        for (int64_t t = blockIdx.x; t < num_tiles && !*abort_v; t += gridDim.x) {
-            const Tile w = tile_at(a, off, parts, t);
-            const int boxes = (w.n + a.box - 1) / a.box;
+    // Warps 0 and 1 run their loops whole, so that addresses and descriptors are uniform over
+    // the warp; one elected lane issues.
+    if (warp == 0) {
+        const bool leader = elect_one();
+        Walk walk(a, off, parts);
+        Tile w;
+        Ring st, sf;
+        uint32_t its = 0, sits = 0;
+        bool ok = true;
+        for (; ok && !*abort_v && walk.tile(w); walk.next()) {
+            const int boxes = w.n <= a.box ? 1 : (w.n + a.box - 1) / a.box;
             const int wrow = w.e * a.N + w.f0;
-            for (int kb = 0; kb < a.num_kb; ++kb, ++it) {
+            const uint32_t w_rows = (uint32_t)((GATE_UP ? 2 : 1) * a.ft);
+            const uint32_t x_rows = (uint32_t)(boxes * a.box);
+            const uint32_t sf_bytes = (w_rows + x_rows) * 16u;
+            const uint32_t st_bytes = w_rows * a.w_count + x_rows * a.x_count;
+            for (int kb = 0; kb < a.num_kb; ++kb) {
                 if (kb % kXSuper == 0) {
-                    const int r = (int)(sit % (uint32_t)R);
-                    if (!mbar_wait(free_bar(r), ((sit / (uint32_t)R) & 1u) ^ 1u, a.status)) {
-                        *abort_v = 1;
-                        break;
+                    ok = mbar_wait(free_bar(sf.at), sf.pass ^ 1u, a.status);
+                    if (!ok) break;
+                    if (leader) {
+                        const uint32_t sl = base + a.sf + (uint32_t)sf.at * a.slot_bytes;
+                        const uint32_t bar = raw_bar(sf.at);
+                        const int x = kb / kXSuper * 16;
+                        mbar_arrive_expect_tx(bar, sf_bytes);
+                        tma_load_2d(sl, &map_w0s, bar, x, wrow);
+                        if (GATE_UP)
+                            tma_load_2d(sl + (uint32_t)a.ft * 16u, &map_w1s, bar, x, wrow);
+                        for (int i = 0; i < boxes; ++i)
+                            tma_load_2d(sl + 2048u + (uint32_t)(i * a.box) * 16u, &map_xs, bar, x,
+                                        w.row0 + i * a.box);
                     }
-                    const uint32_t sl = base + a.sf + (uint32_t)r * a.slot_bytes;
-                    const int x = kb / kXSuper * 16;
-                    mbar_arrive_expect_tx(raw_bar(r),
-                                          (uint32_t)((GATE_UP ? 2 : 1) * a.ft) * 16u +
-                                              (uint32_t)(boxes * a.box) * 16u);
-                    tma_load_2d(sl, &map_w0s, raw_bar(r), x, wrow);
-                    if (GATE_UP)
-                        tma_load_2d(sl + (uint32_t)a.ft * 16u, &map_w1s, raw_bar(r), x, wrow);
+                    sf.next(R);
+                    ++sits;
+                }
+                ok = mbar_wait(empty_bar(st.at), st.pass ^ 1u, a.status);
+                if (!ok) break;
+                if (leader) {
+                    const uint32_t dst = base + a.ring + (uint32_t)st.at * a.stage_bytes;
+                    const uint32_t bar = full_bar(st.at);
+                    const int x = kb * kXBK;
+                    mbar_arrive_expect_tx(bar, st_bytes);
+                    tma_load_2d(dst, &map_w0, bar, x, wrow);
+                    if (GATE_UP) tma_load_2d(dst + (uint32_t)a.ft * 128u, &map_w1, bar, x, wrow);
                     for (int i = 0; i < boxes; ++i)
-                        tma_load_2d(sl + 2048u + (uint32_t)(i * a.box) * 16u, &map_xs, raw_bar(r),
-                                    x, w.row0 + i * a.box);
-                    ++sit;
+                        tma_load_2d(dst + a.a_bytes + (uint32_t)(i * a.box) * 128u, &map_x, bar, x,
+                                    w.row0 + i * a.box);
                 }
-                const int s = (int)(it % (uint32_t)S);
-                if (!mbar_wait(empty_bar(s), ((it / (uint32_t)S) & 1u) ^ 1u, a.status)) {
-                    *abort_v = 1;
-                    break;
-                }
-                const uint32_t st = base + a.ring + (uint32_t)s * a.stage_bytes;
-                mbar_arrive_expect_tx(full_bar(s),
-                                      (uint32_t)((GATE_UP ? 2 : 1) * a.ft) * a.w_count +
-                                          (uint32_t)(boxes * a.box) * a.x_count);
-                tma_load_2d(st, &map_w0, full_bar(s), kb * kXBK, wrow);
-                if (GATE_UP)
-                    tma_load_2d(st + (uint32_t)a.ft * 128u, &map_w1, full_bar(s), kb * kXBK, wrow);
-                for (int i = 0; i < boxes; ++i)
-                    tma_load_2d(st + a.a_bytes + (uint32_t)(i * a.box) * 128u, &map_x, full_bar(s),
-                                kb * kXBK, w.row0 + i * a.box);
+                st.next(S);
+                ++its;
             }
         }
+        if (!ok) *abort_v = 1;
         // Drain: the last loads into every stage and slot have landed before the CTA exits.
-        for (uint32_t i = it > (uint32_t)S ? it - (uint32_t)S : 0u; i < it; ++i)
-            if (!mbar_wait(full_bar((int)(i % (uint32_t)S)), (i / (uint32_t)S) & 1u, a.status))
-                break;
-        for (uint32_t i = sit > (uint32_t)R ? sit - (uint32_t)R : 0u; i < sit; ++i)
-            if (!mbar_wait(raw_bar((int)(i % (uint32_t)R)), (i / (uint32_t)R) & 1u, a.status))
-                break;
-    } else if (warp == 1 && lane == 0) {
-        uint32_t it = 0, sit = 0, j = 0;
+        for (uint32_t i = 0, n = min(its, (uint32_t)S); i < n; ++i) {
+            if (st.at == 0) st.pass ^= 1u;
+            st.at = st.at == 0 ? S - 1 : st.at - 1;
+            if (!mbar_wait(full_bar(st.at), st.pass, a.status)) break;
+        }
+        for (uint32_t i = 0, n = min(sits, (uint32_t)R); i < n; ++i) {
+            if (sf.at == 0) sf.pass ^= 1u;
+            sf.at = sf.at == 0 ? R - 1 : sf.at - 1;
+            if (!mbar_wait(raw_bar(sf.at), sf.pass, a.status)) break;
+        }
+    } else if (warp == 1) {
+        const bool leader = elect_one();
+        Walk walk(a, off, parts);
+        Tile w;
+        Ring st, sf, acc;
+        bool ok = true;
         const uint32_t sf_col = tmem_base + 2u * (uint32_t)a.acc_cols;
-        for (int64_t t = blockIdx.x; t < num_tiles && !*abort_v; t += gridDim.x, ++j) {
-            const Tile w = tile_at(a, off, parts, t);
+        // descriptors: only the start address differs
+        const uint64_t desc0 = sw128_desc(base + a.ring), sdesc0 = scales_desc(base + a.sf);
+        const uint32_t a16 = a.a_bytes >> 4, stage16 = a.stage_bytes >> 4;
+        for (; ok && !*abort_v && walk.tile(w); walk.next()) {
             const uint32_t n8 = (uint32_t)(w.n + 7) & ~7u;
-            const uint32_t b = j & 1u;
-            if (!mbar_wait(tempty_bar((int)b), ((j >> 1) & 1u) ^ 1u, a.status)) {
-                *abort_v = 1;
-                break;
-            }
+            const uint32_t idesc = mx_idesc_at(a.idesc, n8, 0);
+            ok = mbar_wait(tempty_bar(acc.at), acc.pass ^ 1u, a.status);
+            if (!ok) break;
             tc_fence_after();
-            const uint32_t acc = tmem_base + b * (uint32_t)a.acc_cols;
-            for (int kb = 0; kb < a.num_kb; ++kb, ++it) {
-                const int r = (int)(sit % (uint32_t)R);
-                if (kb % kXSuper == 0 &&
-                    !mbar_wait(ready_bar(r), (sit / (uint32_t)R) & 1u, a.status)) {
-                    *abort_v = 1;
-                    break;
+            const uint32_t d = tmem_base + (uint32_t)(acc.at * a.acc_cols);
+            for (int kb = 0; kb < a.num_kb; ++kb) {
+                if (kb % kXSuper == 0) {
+                    ok = mbar_wait(ready_bar(sf.at), sf.pass, a.status);
+                    if (!ok) break;
                 }
-                const int s = (int)(it % (uint32_t)S);
-                if (!mbar_wait(full_bar(s), (it / (uint32_t)S) & 1u, a.status)) {
-                    *abort_v = 1;
-                    break;
-                }
+                ok = mbar_wait(full_bar(st.at), st.pass, a.status);
+                if (!ok) break;
                 tc_fence_after();
                 const uint32_t q = (uint32_t)(kb % kXSuper);
-                const uint32_t sl = base + a.sf + (uint32_t)r * a.slot_bytes + 2048u + a.raw_b;
-                const uint32_t sfa = sf_col + 16u * (q & 1u), sfb = sfa + 4u;
-                tmem_cp_scales(sfa, sl + q * 512u);
-                tmem_cp_scales(sfb, sl + 2048u + q * a.tiled_b);
-                if (n8 > 128u) tmem_cp_scales(sfb + 4u, sl + 2048u + q * a.tiled_b + 512u);
-                const uint32_t st = base + a.ring + (uint32_t)s * a.stage_bytes;
-#pragma unroll
-                for (uint32_t k = 0; k < 4; ++k)
-                    umma_mx(acc, sw128_desc(st + 32u * k), sw128_desc(st + a.a_bytes + 32u * k),
-                            mx_idesc_at(a.idesc, n8, k), sfa, sfb, (kb > 0 || k > 0) ? 1u : 0u);
-                umma_commit(empty_bar(s));
-                if (q == kXSuper - 1 || kb + 1 == a.num_kb) {
-                    umma_commit(free_bar(r));
-                    ++sit;
+                const bool last = q == kXSuper - 1 || kb + 1 == a.num_kb;
+                if (leader) {
+                    const uint64_t sd = sdesc0 + (((uint32_t)sf.at * a.slot_bytes + 2048u + a.raw_b) >> 4);
+                    const uint32_t sfa = sf_col + 16u * (q & 1u), sfb = sfa + 4u;
+                    tmem_cp_scales(sfa, sd + q * 32u);
+                    const uint64_t sdb = sd + 128u + ((q * a.tiled_b) >> 4);
+                    tmem_cp_scales(sfb, sdb);
+                    if (n8 > 128u) tmem_cp_scales(sfb + 4u, sdb + 32u);
+                    const uint64_t ad = desc0 + (uint32_t)st.at * stage16, bd = ad + a16;
+                    umma_mx(d, ad, bd, idesc, sfa, sfb, kb > 0 ? 1u : 0u);
+                    umma_mx(d, ad + 2u, bd + 2u, mx_idesc_at(idesc, 0, 1), sfa, sfb, 1u);
+                    umma_mx(d, ad + 4u, bd + 4u, mx_idesc_at(idesc, 0, 2), sfa, sfb, 1u);
+                    umma_mx(d, ad + 6u, bd + 6u, mx_idesc_at(idesc, 0, 3), sfa, sfb, 1u);
+                    umma_commit(empty_bar(st.at));
+                    if (last) umma_commit(free_bar(sf.at));
+                    if (kb + 1 == a.num_kb) umma_commit(tfull_bar(acc.at));
                 }
+                st.next(S);
+                if (last) sf.next(R);
             }
-            if (*abort_v) break;
-            umma_commit(tfull_bar((int)b));
+            acc.next(2);
         }
+        if (!ok) *abort_v = 1;
         // Every MMA and copy issued above has completed before the columns are freed.
-        umma_commit(drain_bar);
+        if (leader) umma_commit(drain_bar);
         mbar_wait(drain_bar, 0u, a.status);
     } else if (warp == 2 || warp == 3) {
-        uint32_t sit = 0;
+        Walk walk(a, off, parts);
+        Tile w;
+        Ring sf;
         const int supers = (a.num_kb + kXSuper - 1) / kXSuper;
         bool ok = true;
-        for (int64_t t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
-            const Tile w = tile_at(a, off, parts, t);
-            // 32-row pieces in which each quarter-warp's 8 rows lie 32 rows apart, so that
-            // a warp's 32 words fill 128 contiguous bytes of a tile.
-            const int pa = 4, pb = (w.n + 127) / 128 * 4;
-            for (int c = 0; c < supers; ++c, ++sit) {
-                const int r = (int)(sit % (uint32_t)R);
+        // The row of a lane in a 32-row piece i of 128 rows, and its place in the 512-byte tile:
+        // a quarter-warp's 8 rows lie 32 rows from the next one's, so that the warp's 32 words
+        // fill 128 contiguous bytes.
+        const int row0 = (lane & 7) + 32 * (lane >> 3);
+        const int dst0 = (lane & 7) * 16 + (lane >> 3) * 4;
+        for (; ok && walk.tile(w); walk.next()) {
+            const int pb = w.n <= 128 ? 4 : 8;
+            for (int c = 0; c < supers; ++c) {
                 ok = __all_sync(MOE_FULL_MASK,
-                                !*abort_v &&
-                                    mbar_wait(raw_bar(r), (sit / (uint32_t)R) & 1u, a.status));
-                if (!ok) {
-                    if (lane == 0) *abort_v = 1;
-                    break;
-                }
-                uint8_t *sl = gbase + a.sf + (size_t)r * a.slot_bytes;
-                for (int i = warp - 2; i < pa + pb; i += 2) {
-                    const bool is_b = i >= pa;
-                    const int p = is_b ? i - pa : i;
-                    // row in its group of 128, and its place in the 512-byte tile
-                    const int row = 8 * (p & 3) + (lane & 7) + 32 * (lane >> 3);
-                    const int g = p >> 2;
-                    if (is_b && g * 128 + row >= (int)(a.raw_b >> 4)) continue;
-                    const uint4 v = *reinterpret_cast<const uint4 *>(
-                        sl + (is_b ? 2048 : 0) + (g * 128 + row) * 16);
-                    uint8_t *dst = sl + 2048 + a.raw_b + (is_b ? 2048 + g * 512 : 0) +
-                                   (row & 31) * 16 + (row >> 5) * 4;
-                    const uint32_t step = is_b ? a.tiled_b : 512u;
-                    *reinterpret_cast<uint32_t *>(dst) = v.x;
-                    *reinterpret_cast<uint32_t *>(dst + step) = v.y;
-                    *reinterpret_cast<uint32_t *>(dst + 2 * step) = v.z;
-                    *reinterpret_cast<uint32_t *>(dst + 3 * step) = v.w;
-                }
+                                !*abort_v && mbar_wait(raw_bar(sf.at), sf.pass, a.status));
+                if (!ok) break;
+                uint8_t *sl = gbase + a.sf + (size_t)sf.at * a.slot_bytes;
+                // warp 2 turns the pieces 0, 2, .. and warp 3 the others
+                turn_scales(sl, sl + 2048 + a.raw_b, 512, warp - 2, 4, 128, row0, dst0);
+                turn_scales(sl + 2048, sl + 4096 + a.raw_b, (int)a.tiled_b, warp - 2, pb, a.cap,
+                            row0, dst0);
                 fence_async_shared();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(ready_bar(r));
+                if (lane == 0) mbar_arrive(ready_bar(sf.at));
+                sf.next(R);
             }
         }
+        if (!ok) *abort_v = 1;
     } else if (warp >= 4) {
-        const int q = warp & 3;
+        // Two warps share a quarter of the TMEM lanes, half of a chunk's columns each.
+        const int q = warp & 3, half = (warp - 4) >> 2;
+        const int tid = (int)threadIdx.x - 128;
         float *stg = reinterpret_cast<float *>(gbase + a.stg);
-        uint32_t j = 0;
-        for (int64_t t = blockIdx.x; t < num_tiles; t += gridDim.x, ++j) {
-            const Tile w = tile_at(a, off, parts, t);
-            const uint32_t b = j & 1u;
+        Walk walk(a, off, parts);
+        Tile w;
+        Ring acc;
+        // 8-feature groups of a token: a thread keeps its group (8 or 16 of them a tile).
+        const int shift = a.ft == 128 ? 4 : a.ft == 64 ? 3 : 2;
+        const int grp = tid & ((1 << shift) - 1), tok0 = tid >> shift, tok_step = kXEpiThreads >> shift;
+        for (; walk.tile(w); walk.next()) {
             // Every epilogue thread goes by the same answer: they meet at the barriers below.
-            int ok = !*abort_v && mbar_wait(tfull_bar((int)b), (j >> 1) & 1u, a.status);
+            int ok = !*abort_v && mbar_wait(tfull_bar(acc.at), acc.pass, a.status);
             asm volatile(
                 "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %0, 0;\n\t"
                 "barrier.red.and.pred q, 1, %1, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
@@ -338,91 +430,70 @@ __global__ void __launch_bounds__(kXThreads, 1)
                 : "n"(kXEpiThreads)
                 : "memory");
             if (!ok) {
-                if (lane == 0) *abort_v = 1;
+                *abort_v = 1;
                 break;
             }
             tc_fence_after();
-            const uint32_t trow =
-                tmem_base + b * (uint32_t)a.acc_cols + ((uint32_t)(q * 32) << 16);
-            const int64_t brow = (int64_t)w.e * a.N;
-            // 8-feature groups of a token; gate_up's last tile adds those of the row's padding.
-            const int own = a.ft >> 3;
-            const int padded = (a.N + kMxPad - 1) / kMxPad * kMxPad;
-            const int groups = GATE_UP && w.f0 + a.ft >= a.N ? (padded - w.f0) >> 3 : own;
+            const uint32_t trow = tmem_base + (uint32_t)(acc.at * a.acc_cols) +
+                                  ((uint32_t)(q * 32) << 16) + (uint32_t)(16 * half);
+            const int f = w.f0 + 8 * grp;
+            const bool real_f = f < a.N;
+            float b0[8], b1[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) b0[k] = b1[k] = 0.0f;
+            if (real_f && a.bias0) load8(a.bias0 + (int64_t)w.e * a.N + f, b0);
+            if (GATE_UP && real_f && a.bias1) load8(a.bias1 + (int64_t)w.e * a.N + f, b1);
             for (int c0 = 0; c0 < w.n; c0 += kXChunk) {
-                uint32_t v[kXChunk];
-                tmem_ld32(trow + (uint32_t)c0, v);
+                uint32_t v[16];
+                tmem_ld16(trow + (uint32_t)c0, v);
                 if (c0 + kXChunk >= w.n) {  // the accumulator is free for the tile after next
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(tempty_bar((int)b));
+                    if (lane == 0) mbar_arrive(tempty_bar(acc.at));
                 }
                 epi_sync();  // the last chunk's readers are done
 #pragma unroll
-                for (int i = 0; i < kXChunk; ++i)
-                    stg[i * kXPitch + 32 * q + lane] = __uint_as_float(v[i]);
+                for (int i = 0; i < 16; ++i)
+                    stg[(16 * half + i) * kXPitch + 32 * q + lane] = __uint_as_float(v[i]);
                 epi_sync();
-                const int items = min(kXChunk, w.n - c0) * groups;
-                for (int i0 = 32 * q; i0 < items; i0 += kXEpiThreads) {
-                    const int i = i0 + lane;
-                    const int tok = i / groups, grp = i - tok * groups;
-                    const int f = w.f0 + 8 * grp;
-                    const bool there = i < items, real = there && grp < own && f < a.N;
+                const int left = w.n - c0;
+                // whole warps go on while any of their tokens is there (the block's shuffles)
+                for (int tok = tok0; tok < kXChunk; tok += tok_step) {
+                    const bool there = tok < left;
+                    if (!__any_sync(MOE_FULL_MASK, there)) break;
                     const int64_t row = (int64_t)w.row0 + c0 + tok;
+                    const float *src = stg + tok * kXPitch + 8 * grp;
                     float o[8];
+                    load8(src, o);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) o[k] = 0.0f;
-                    if (real) {
-                        const float *src = stg + tok * kXPitch + 8 * grp;
-#pragma unroll
-                        for (int k = 0; k < 8; k += 4) {
-                            const float4 g = *reinterpret_cast<const float4 *>(src + k);
-                            float4 b0 = make_float4(0.f, 0.f, 0.f, 0.f), b1 = b0;
-                            if (a.bias0)
-                                b0 = __ldg(reinterpret_cast<const float4 *>(a.bias0 + brow + f + k));
-                            o[k] = g.x + b0.x;
-                            o[k + 1] = g.y + b0.y;
-                            o[k + 2] = g.z + b0.z;
-                            o[k + 3] = g.w + b0.w;
-                            if (GATE_UP) {
-                                const float4 u =
-                                    *reinterpret_cast<const float4 *>(src + a.ft + k);
-                                if (a.bias1)
-                                    b1 = __ldg(
-                                        reinterpret_cast<const float4 *>(a.bias1 + brow + f + k));
-                                o[k] = activate(o[k], u.x + b1.x, a.act);
-                                o[k + 1] = activate(o[k + 1], u.y + b1.y, a.act);
-                                o[k + 2] = activate(o[k + 2], u.z + b1.z, a.act);
-                                o[k + 3] = activate(o[k + 3], u.w + b1.w, a.act);
-                            }
-                        }
-                    }
+                    for (int k = 0; k < 8; ++k) o[k] += b0[k];
                     if (GATE_UP) {
-                        uint32_t byte;
-                        uint8_t *srow = a.hs + row * a.h_scale;
-                        if (a.h_fmt == MOE_MX_E4M3) {
-                            const uint2 e = mx_quarter<MOE_MX_E4M3>(o, byte);
-                            if (there)
-                                mx_store<MOE_MX_E4M3>(a.hq + row * a.h_row, srow, f >> 3, e, byte);
-                        } else {
-                            const uint2 e = mx_quarter<MOE_MX_E2M1>(o, byte);
-                            if (there)
-                                mx_store<MOE_MX_E2M1>(a.hq + row * a.h_row, srow, f >> 3, e, byte);
-                        }
-                        if (there && f + 8 == padded)
-                            for (int64_t k = padded / kMxBlock; k < a.h_scale; ++k) srow[k] = 0;
-                    } else if (real) {
-                        uint32_t p[4];
+                        float u[8];
+                        load8(src + a.ft, u);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const __nv_bfloat162 two = __floats2bfloat162_rn(o[2 * k], o[2 * k + 1]);
-                            p[k] = *reinterpret_cast<const uint32_t *>(&two);
-                        }
-                        *reinterpret_cast<uint4 *>(a.y + row * a.N + f) =
-                            make_uint4(p[0], p[1], p[2], p[3]);
+                        for (int k = 0; k < 8; ++k) u[k] += b1[k];
+                        activate8(o, u, a.act);
+                        // features behind N: zeros of the row's padding
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) o[k] = real_f && there ? o[k] : 0.0f;
+                        store_h(a, row, f, o, there);
+                    } else if (there && real_f) {
+                        *reinterpret_cast<uint4 *>(a.y + row * a.N + f) = pack_bf16x8(o);
                     }
                 }
             }
+            // The last feature tile's tokens get what is left of their rows' padding.
+            if (GATE_UP && w.f0 + a.ft >= a.N) {
+                for (int i = tid; i < w.n; i += kXEpiThreads) {
+                    const int64_t row = (int64_t)w.row0 + i;
+                    uint8_t *qrow = a.hq + row * a.h_row, *srow = a.hs + row * a.h_scale;
+                    const int64_t from = a.h_fmt == MOE_MX_E4M3 ? w.f0 + a.ft : (w.f0 + a.ft) / 2;
+                    for (int64_t k = from; k < a.h_row; k += 16)
+                        *reinterpret_cast<uint4 *>(qrow + k) = make_uint4(0u, 0u, 0u, 0u);
+                    for (int64_t k = (w.f0 + a.ft) / kMxBlock; k < a.h_scale; ++k) srow[k] = 0;
+                }
+            }
+            acc.next(2);
         }
     }
 
@@ -450,7 +521,7 @@ moe_status launch_expert_mx(const uint8_t *xq, const uint8_t *xs, int32_t x_fmt,
     // memory to more weight stages.
     const int64_t share = 4 * ((a.rows + a.E - 1) / a.E);
     a.cap = share <= 32 ? 32 : share <= 64 ? 64 : share <= 128 ? 128 : 224;
-    a.box = a.cap <= 64 ? 8 : 32;
+    a.box = a.cap / 2;  // one or two loads a stage
     a.acc_cols = a.cap;
     a.ft = GATE_UP ? 64 : 128;
     a.f_tiles = (a.N + a.ft - 1) / a.ft;
@@ -525,9 +596,8 @@ moe_status check_ffn_mx(const void *x, const void *xs, int32_t x_fmt, int32_t w_
         return MOE_ERR_INVALID_ARG;
     if (rows == 0) return MOE_OK;
     if (!x || !xs || !offsets || !mx_aligned(x, xs)) return MOE_ERR_INVALID_ARG;
-    if (d > kMxMaxK || F > kMxMaxK || rows >= (int64_t)INT32_MAX - 512 ||
-        (int64_t)E * (d > F ? d : F) >= (int64_t)INT32_MAX - 512)
-        return MOE_ERR_UNSUPPORTED;
+    // Row coordinates stay below 2^31 with a tile's overhang (E rows of weights: at most 2^30).
+    if (d > kMxMaxK || F > kMxMaxK || rows >= (int64_t)INT32_MAX - 512) return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
 }
 
