@@ -16,17 +16,20 @@
 // A persistent grid walks tiles (block part, feature tile), features fastest:
 // CTAs that run together share their tokens, and an expert's weights stay in
 // L2 over its parts.  Roles of a CTA:
-//   warp 0     TMA: weight and token tiles of 128 K values into a stage ring;
-//              scale rows, 16 bytes (512 K values) at a time, into a second ring
-//   warps 2, 3 turn raw scale rows [row][16 bytes] into the tiles that TMEM
+//   warp 0     TMA: weight and token tiles of 128 K values into a stage ring
+//   warp 2     TMA: scale rows, 16 bytes (512 K values) at a time, into a second ring
+//   warp 3     turns raw scale rows [row][16 bytes] into the tiles that TMEM
 //              wants (32 x 16 bytes, four rows' words side by side)
-//   warp 1     one thread: scale tiles to TMEM (tcgen05.cp), four MMAs a stage
+//   warp 1     scale tiles to TMEM (tcgen05.cp) and four MMAs for every 128 K values
 //   warps 4-11 epilogue: TMEM -> shared memory, transposed to token-major; each
 //              thread then takes 8 features of a token: bias, activation, MX
 //              block (four lanes) or bf16, and one vector store
 // Two accumulators: the epilogue of a tile overlaps the next one's products.
 // A gate_up tile has ft gate rows and the ft up rows of the same features in
 // its 128 rows; they meet in the epilogue's shared memory.
+//
+// PAIR: two CTAs on two SMs (cta_group::2) hold one token tile: each has its
+// own 128 weight rows, half of the tokens' rows, and all of the tokens' scales.
 // Every wait is bounded, as in the bf16 kernels.
 #include "mx.cuh"
 #include "rows.cuh"
@@ -39,9 +42,16 @@ constexpr int kXThreads = 384;
 constexpr int kXBK = 128;           // K values of a stage
 constexpr int kXSuper = 4;          // stages that one load of scales covers
 constexpr int kXMaxE = 4096;
+constexpr int kXMaxStages = 12;
 constexpr int kXEpiThreads = 256;
-constexpr int kXChunk = 32;         // token columns the epilogue turns at a time
-constexpr int kXPitch = 132;        // floats of a staged token: 16-byte aligned, off the banks
+constexpr int kXChunk = 32;         // token columns the epilogue turns at a time,
+constexpr int kXChunkHalf = 16;     // half of them by each of a quarter's two warps
+// Floats of a staged token: 16-byte aligned, the rows of eight reading lanes on different banks.
+// gate_up: 32 gate and 32 up values, two buffers of 16 tokens for each of the 4 pairs of warps;
+// down: 32 values, one buffer for each of the 8 warps.
+constexpr int kXPitch[2] = {36, 68};
+constexpr int kXBuffer[2] = {16 * 36, 16 * 68};
+constexpr int kXStageBytes[2] = {8 * 16 * 36 * 4, 4 * 2 * 16 * 68 * 4};
 constexpr float kXOaiAlpha = 1.702f;
 constexpr float kXOaiLimit = 7.0f;
 
@@ -54,10 +64,17 @@ struct MxFfnArgs {
     int64_t h_row, h_scale;  // bytes of those rows
     int32_t *status;
     int64_t rows;
-    int E, N, ft, f_tiles, cap, acc_cols, box, num_kb, stages, slots, tmem_cols, act, h_fmt;
-    uint32_t w_count, x_count;  // bytes a barrier counts for a row of a stage: 4-bit values packed
-    uint32_t a_bytes, stage_bytes, raw_b, tiled_b, slot_bytes, idesc;
-    uint32_t ring, sf, stg, bars, tables;  // offsets in shared memory
+    int E, N;
+    int ft;                  // features of a CTA's tile
+    int f_tiles;             // tiles (of a CTA or a pair) that cover the features
+    int cap;                 // most tokens of a tile; also the columns of an accumulator
+    int ks;                  // 128-value K blocks of a stage
+    int num_kb, stages, slots, tmem_cols, act, h_fmt;
+    uint32_t a_bytes, b_bytes;     // a K block's weight and token tile in shared memory
+    uint32_t stage_bytes;          // ks of both
+    uint32_t stage_tx, slot_tx;    // bytes their barriers count: 4-bit values packed
+    uint32_t raw_b, tiled_b, slot_bytes, idesc;
+    uint32_t sf, stg, bars, tables;  // offsets in shared memory (the stages come first)
 };
 
 // As in the bf16 kernel's epilogue: fast exponential and quotient, about 1e-6
@@ -97,19 +114,22 @@ __device__ __forceinline__ void store_h(const MxFfnArgs &a, int64_t row, int f, 
     }
 }
 
-// Raw scale rows (16 bytes: four stages' words) to the four stages' tiles, `step` bytes apart:
-// every second of `pieces` 32-row pieces, rows below `rows`.
-__device__ __forceinline__ void turn_scales(const uint8_t *raw, uint8_t *tiles, int step, int first,
-                                            int pieces, int rows, int row0, int dst0) {
-    for (int i = first; i < pieces; i += 2) {
-        const int r = (i >> 2) * 128 + 8 * (i & 3) + row0;
-        if (r >= rows) continue;
-        const uint4 v = *reinterpret_cast<const uint4 *>(raw + r * 16);
-        uint8_t *dst = tiles + (i >> 2) * 512 + (i & 3) * 128 + dst0;
-        *reinterpret_cast<uint32_t *>(dst) = v.x;
-        *reinterpret_cast<uint32_t *>(dst + step) = v.y;
-        *reinterpret_cast<uint32_t *>(dst + 2 * step) = v.z;
-        *reinterpret_cast<uint32_t *>(dst + 3 * step) = v.w;
+// Raw scale rows of up to 128 operand rows (16 bytes each: four K blocks' words) to the four
+// blocks' 512-byte tiles, `step` bytes apart.  A lane's row in piece i is 8 i + lane % 8 +
+// 32 (lane / 8): the warp's 32 words of a block then fill 128 contiguous bytes.
+__device__ __forceinline__ void turn_scales(const uint8_t *raw, uint8_t *tiles, uint32_t step,
+                                            int lane) {
+    const uint4 *src = reinterpret_cast<const uint4 *>(raw) + (lane & 7) + 32 * (lane >> 3);
+    uint4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = src[8 * i];
+    uint8_t *dst = tiles + (lane & 7) * 16 + (lane >> 3) * 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        *reinterpret_cast<uint32_t *>(dst + 128 * i) = v[i].x;
+        *reinterpret_cast<uint32_t *>(dst + 128 * i + step) = v[i].y;
+        *reinterpret_cast<uint32_t *>(dst + 128 * i + 2 * step) = v[i].z;
+        *reinterpret_cast<uint32_t *>(dst + 128 * i + 3 * step) = v[i].w;
     }
 }
 
@@ -117,20 +137,23 @@ struct Tile {
     int e, row0, n, f0;
 };
 
-// The tiles of one CTA in order: tile t = part * f_tiles + feature tile, t = blockIdx.x,
-// + gridDim.x, ...  Every role of the CTA walks them.  The quotients are carried along:
+// The tiles of a CTA (or pair) in order: tile t = part * f_tiles + feature tile, t = its number,
+// + their number, ...  Every role of the CTA walks them.  The quotients are carried along:
 // a runtime division in a role's loop costs as much as issuing a stage.
 struct Walk {
     const int32_t *off, *parts;
-    int E, ft, f_tiles, step_p, step_f;
+    int E, f_step, f_first, f_tiles, step_p, step_f;
     int p, f, e;
 
-    __device__ __forceinline__ Walk(const MxFfnArgs &a, const int32_t *o, const int32_t *q)
-        : off(o), parts(q), E(a.E), ft(a.ft), f_tiles(a.f_tiles) {
-        step_p = (int)gridDim.x / f_tiles;
-        step_f = (int)gridDim.x - step_p * f_tiles;
-        p = (int)blockIdx.x / f_tiles;
-        f = (int)blockIdx.x - p * f_tiles;
+    // ctas: CTAs that walk as one (1, or 2 of which this is number `rank`).
+    __device__ __forceinline__ Walk(const MxFfnArgs &a, const int32_t *o, const int32_t *q,
+                                    int ctas, int rank)
+        : off(o), parts(q), E(a.E), f_step(ctas * a.ft), f_first(rank * a.ft), f_tiles(a.f_tiles) {
+        const int unit = (int)blockIdx.x / ctas, units = (int)gridDim.x / ctas;
+        step_p = units / f_tiles;
+        step_f = units - step_p * f_tiles;
+        p = unit / f_tiles;
+        f = unit - p * f_tiles;
         e = 0;
     }
     __device__ __forceinline__ void next() {
@@ -159,7 +182,7 @@ struct Walk {
         w.e = e;
         w.row0 = first + (p - parts[e]) * share;
         w.n = min(share, first + m - w.row0);
-        w.f0 = f * ft;
+        w.f0 = f * f_step + f_first;
         return true;
     }
 };
@@ -174,13 +197,15 @@ struct Ring {
             pass ^= 1u;
         }
     }
+    __device__ __forceinline__ void back(int size) {
+        if (at-- == 0) {
+            at = size - 1;
+            pass ^= 1u;
+        }
+    }
 };
 
-__device__ __forceinline__ void epi_sync() {
-    asm volatile("bar.sync 1, %0;" ::"n"(kXEpiThreads) : "memory");
-}
-
-template <bool GATE_UP>
+template <bool GATE_UP, bool PAIR>
 __global__ void __launch_bounds__(kXThreads, 1)
     expert_mx_kernel(const __grid_constant__ CUtensorMap map_w0,
                      const __grid_constant__ CUtensorMap map_w1,
@@ -190,19 +215,21 @@ __global__ void __launch_bounds__(kXThreads, 1)
                      const __grid_constant__ CUtensorMap map_xs, const MxFfnArgs a) {
     extern __shared__ __align__(16) uint8_t smem_mx[];
     __shared__ int abort_s;
+    constexpr int kCtas = PAIR ? 2 : 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = PAIR ? (int)cluster_cta_rank() : 0;
     const uint32_t raw = smem_u32(smem_mx);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t *const gbase = smem_mx + (base - raw);
     const int S = a.stages, R = a.slots;
     const uint32_t bar0 = base + a.bars;
-    auto full_bar = [&](int s) { return bar0 + 8u * s; };
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };                   // the leader's
     auto empty_bar = [&](int s) { return bar0 + 8u * (S + s); };
     auto raw_bar = [&](int r) { return bar0 + 8u * (2 * S + r); };
-    auto ready_bar = [&](int r) { return bar0 + 8u * (2 * S + R + r); };
+    auto ready_bar = [&](int r) { return bar0 + 8u * (2 * S + R + r); };    // the leader's
     auto free_bar = [&](int r) { return bar0 + 8u * (2 * S + 2 * R + r); };
     auto tfull_bar = [&](int b) { return bar0 + 8u * (2 * S + 3 * R + b); };
-    auto tempty_bar = [&](int b) { return bar0 + 8u * (2 * S + 3 * R + 2 + b); };
+    auto tempty_bar = [&](int b) { return bar0 + 8u * (2 * S + 3 * R + 2 + b); };  // the leader's
     const uint32_t drain_bar = bar0 + 8u * (2 * S + 3 * R + 4);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + a.bars + 8u * (2 * S + 3 * R + 5));
     int32_t *off = reinterpret_cast<int32_t *>(gbase + a.tables);
@@ -216,27 +243,40 @@ __global__ void __launch_bounds__(kXThreads, 1)
         }
         for (int r = 0; r < R; ++r) {
             mbar_init(raw_bar(r), 1);
-            mbar_init(ready_bar(r), 2);  // one arrival per turning warp
+            mbar_init(ready_bar(r), kCtas);  // each CTA's turning warp
             mbar_init(free_bar(r), 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(tfull_bar(b), 1);
-            mbar_init(tempty_bar(b), 8);  // one arrival per epilogue warp
+            mbar_init(tempty_bar(b), 8 * kCtas);  // each CTA's epilogue warps
         }
         mbar_init(drain_bar, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 2) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                         smem_u32(tmem_slot)),
-                     "r"(a.tmem_cols)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        if (PAIR) {
+            asm volatile(
+                "tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                    smem_u32(tmem_slot)),
+                "r"(a.tmem_cols)
+                : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        } else {
+            asm volatile(
+                "tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                    smem_u32(tmem_slot)),
+                "r"(a.tmem_cols)
+                : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        }
     }
     griddep_wait();  // offsets and tokens come from the kernels before this one
     for (int i = threadIdx.x; i <= a.E; i += blockDim.x) off[i] = __ldg(a.offsets + i);
     tc_fence_before();
-    __syncthreads();
+    if (PAIR)
+        cluster_sync();
+    else
+        __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     // Blocks that descend or leave the buffers: nothing runs.
@@ -264,165 +304,229 @@ __global__ void __launch_bounds__(kXThreads, 1)
     volatile int *abort_v = &abort_s;
     griddep_launch_dependents();
 
-    // Warps 0 and 1 run their loops whole, so that addresses and descriptors are uniform over
+    // Warps 0 to 3 run their loops whole, so that addresses and descriptors are uniform over
     // the warp; one elected lane issues.
     if (warp == 0) {
         const bool leader = elect_one();
-        Walk walk(a, off, parts);
+        Walk walk(a, off, parts, kCtas, rank);
         Tile w;
-        Ring st, sf;
-        uint32_t its = 0, sits = 0;
+        Ring st;
+        uint32_t filled = 0;
         bool ok = true;
+        const uint32_t lead_full = PAIR ? cluster_map(full_bar(0), 0) : full_bar(0);
         for (; ok && !*abort_v && walk.tile(w); walk.next()) {
-            const int boxes = w.n <= a.box ? 1 : (w.n + a.box - 1) / a.box;
             const int wrow = w.e * a.N + w.f0;
-            const uint32_t w_rows = (uint32_t)((GATE_UP ? 2 : 1) * a.ft);
-            const uint32_t x_rows = (uint32_t)(boxes * a.box);
-            const uint32_t sf_bytes = (w_rows + x_rows) * 16u;
-            const uint32_t st_bytes = w_rows * a.w_count + x_rows * a.x_count;
-            for (int kb = 0; kb < a.num_kb; ++kb) {
-                if (kb % kXSuper == 0) {
-                    ok = mbar_wait(free_bar(sf.at), sf.pass ^ 1u, a.status);
-                    if (!ok) break;
-                    if (leader) {
-                        const uint32_t sl = base + a.sf + (uint32_t)sf.at * a.slot_bytes;
-                        const uint32_t bar = raw_bar(sf.at);
-                        const int x = kb / kXSuper * 16;
-                        mbar_arrive_expect_tx(bar, sf_bytes);
-                        tma_load_2d(sl, &map_w0s, bar, x, wrow);
-                        if (GATE_UP)
-                            tma_load_2d(sl + (uint32_t)a.ft * 16u, &map_w1s, bar, x, wrow);
-                        for (int i = 0; i < boxes; ++i)
-                            tma_load_2d(sl + 2048u + (uint32_t)(i * a.box) * 16u, &map_xs, bar, x,
-                                        w.row0 + i * a.box);
-                    }
-                    sf.next(R);
-                    ++sits;
-                }
+            // a pair's tokens in multiples of 16: each CTA holds one half's rows
+            const int xrow = w.row0 + (PAIR ? rank * (((w.n + 15) & ~15) >> 1) : 0);
+            for (int kb = 0; kb < a.num_kb; kb += a.ks) {
                 ok = mbar_wait(empty_bar(st.at), st.pass ^ 1u, a.status);
                 if (!ok) break;
                 if (leader) {
-                    const uint32_t dst = base + a.ring + (uint32_t)st.at * a.stage_bytes;
-                    const uint32_t bar = full_bar(st.at);
-                    const int x = kb * kXBK;
-                    mbar_arrive_expect_tx(bar, st_bytes);
-                    tma_load_2d(dst, &map_w0, bar, x, wrow);
-                    if (GATE_UP) tma_load_2d(dst + (uint32_t)a.ft * 128u, &map_w1, bar, x, wrow);
-                    for (int i = 0; i < boxes; ++i)
-                        tma_load_2d(dst + a.a_bytes + (uint32_t)(i * a.box) * 128u, &map_x, bar, x,
-                                    w.row0 + i * a.box);
+                    uint32_t dst = base + (uint32_t)st.at * a.stage_bytes;
+                    const uint32_t bar = lead_full + 8u * (uint32_t)st.at;
+                    if (rank == 0) mbar_arrive_expect_tx(full_bar(st.at), a.stage_tx);
+                    // K blocks behind the last are filled with zeros (and not multiplied)
+                    if (GATE_UP) {
+                        for (int i = 0; i < a.ks; ++i) {
+                            if (PAIR) {
+                                tma_load_3d_pair(dst, &map_w0, bar, 0, wrow, kb + i);
+                                tma_load_3d_pair(dst + (uint32_t)a.ft * 128u, &map_w1, bar, 0, wrow,
+                                                 kb + i);
+                            } else {
+                                tma_load_3d(dst, &map_w0, bar, 0, wrow, kb + i);
+                                tma_load_3d(dst + (uint32_t)a.ft * 128u, &map_w1, bar, 0, wrow,
+                                            kb + i);
+                            }
+                            dst += a.a_bytes;
+                        }
+                    } else {
+                        if (PAIR)
+                            tma_load_3d_pair(dst, &map_w0, bar, 0, wrow, kb);
+                        else
+                            tma_load_3d(dst, &map_w0, bar, 0, wrow, kb);
+                        dst += (uint32_t)a.ks * a.a_bytes;
+                    }
+                    if (PAIR)
+                        tma_load_3d_pair(dst, &map_x, bar, 0, xrow, kb);
+                    else
+                        tma_load_3d(dst, &map_x, bar, 0, xrow, kb);
                 }
                 st.next(S);
-                ++its;
+                ++filled;
             }
         }
         if (!ok) *abort_v = 1;
-        // Drain: the last loads into every stage and slot have landed before the CTA exits.
-        for (uint32_t i = 0, n = min(its, (uint32_t)S); i < n; ++i) {
-            if (st.at == 0) st.pass ^= 1u;
-            st.at = st.at == 0 ? S - 1 : st.at - 1;
+        // Drain (the leader's barriers count both CTAs' bytes): the last loads into every stage
+        // have landed before the CTAs exit.
+        for (uint32_t i = 0, n = rank == 0 ? min(filled, (uint32_t)S) : 0u; i < n; ++i) {
+            st.back(S);
             if (!mbar_wait(full_bar(st.at), st.pass, a.status)) break;
         }
-        for (uint32_t i = 0, n = min(sits, (uint32_t)R); i < n; ++i) {
-            if (sf.at == 0) sf.pass ^= 1u;
-            sf.at = sf.at == 0 ? R - 1 : sf.at - 1;
-            if (!mbar_wait(raw_bar(sf.at), sf.pass, a.status)) break;
-        }
     } else if (warp == 1) {
-        const bool leader = elect_one();
-        Walk walk(a, off, parts);
-        Tile w;
-        Ring st, sf, acc;
-        bool ok = true;
-        const uint32_t sf_col = tmem_base + 2u * (uint32_t)a.acc_cols;
-        // descriptors: only the start address differs
-        const uint64_t desc0 = sw128_desc(base + a.ring), sdesc0 = scales_desc(base + a.sf);
-        const uint32_t a16 = a.a_bytes >> 4, stage16 = a.stage_bytes >> 4;
-        for (; ok && !*abort_v && walk.tile(w); walk.next()) {
-            const uint32_t n8 = (uint32_t)(w.n + 7) & ~7u;
-            const uint32_t idesc = mx_idesc_at(a.idesc, n8, 0);
-            ok = mbar_wait(tempty_bar(acc.at), acc.pass ^ 1u, a.status);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t d = tmem_base + (uint32_t)(acc.at * a.acc_cols);
-            for (int kb = 0; kb < a.num_kb; ++kb) {
-                if (kb % kXSuper == 0) {
-                    ok = mbar_wait(ready_bar(sf.at), sf.pass, a.status);
-                    if (!ok) break;
-                }
-                ok = mbar_wait(full_bar(st.at), st.pass, a.status);
+        if (rank == 0) {
+            const bool leader = elect_one();
+            Walk walk(a, off, parts, kCtas, rank);
+            Tile w;
+            Ring st, sf, acc;
+            bool ok = true;
+            const uint32_t sf_col = tmem_base + 2u * (uint32_t)a.cap;
+            // descriptors: only the start address differs
+            const uint64_t desc0 = sw128_desc(base), sdesc0 = scales_desc(base + a.sf + 2048u + a.raw_b);
+            const uint32_t a16 = a.a_bytes >> 4, b16 = a.b_bytes >> 4;
+            for (; ok && !*abort_v && walk.tile(w); walk.next()) {
+                const uint32_t n = PAIR ? (uint32_t)(w.n + 15) & ~15u : (uint32_t)(w.n + 7) & ~7u;
+                const uint32_t idesc = mx_idesc_at(a.idesc, n, 0);
+                ok = mbar_wait(tempty_bar(acc.at), acc.pass ^ 1u, a.status);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t q = (uint32_t)(kb % kXSuper);
-                const bool last = q == kXSuper - 1 || kb + 1 == a.num_kb;
-                if (leader) {
-                    const uint64_t sd = sdesc0 + (((uint32_t)sf.at * a.slot_bytes + 2048u + a.raw_b) >> 4);
-                    const uint32_t sfa = sf_col + 16u * (q & 1u), sfb = sfa + 4u;
-                    tmem_cp_scales(sfa, sd + q * 32u);
-                    const uint64_t sdb = sd + 128u + ((q * a.tiled_b) >> 4);
-                    tmem_cp_scales(sfb, sdb);
-                    if (n8 > 128u) tmem_cp_scales(sfb + 4u, sdb + 32u);
-                    const uint64_t ad = desc0 + (uint32_t)st.at * stage16, bd = ad + a16;
-                    umma_mx(d, ad, bd, idesc, sfa, sfb, kb > 0 ? 1u : 0u);
-                    umma_mx(d, ad + 2u, bd + 2u, mx_idesc_at(idesc, 0, 1), sfa, sfb, 1u);
-                    umma_mx(d, ad + 4u, bd + 4u, mx_idesc_at(idesc, 0, 2), sfa, sfb, 1u);
-                    umma_mx(d, ad + 6u, bd + 6u, mx_idesc_at(idesc, 0, 3), sfa, sfb, 1u);
-                    umma_commit(empty_bar(st.at));
-                    if (last) umma_commit(free_bar(sf.at));
-                    if (kb + 1 == a.num_kb) umma_commit(tfull_bar(acc.at));
+                const uint32_t d = tmem_base + (uint32_t)(acc.at * a.cap);
+                for (int kb0 = 0; kb0 < a.num_kb; kb0 += a.ks) {
+                    if (kb0 % kXSuper == 0) {
+                        ok = mbar_wait(ready_bar(sf.at), sf.pass, a.status);
+                        if (!ok) break;
+                    }
+                    ok = mbar_wait(full_bar(st.at), st.pass, a.status);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const int kb1 = min(kb0 + a.ks, a.num_kb);
+                    const bool last = kb1 % kXSuper == 0 || kb1 == a.num_kb;
+                    if (leader) {
+                        const uint32_t stage16 = ((uint32_t)st.at * a.stage_bytes) >> 4;
+                        uint64_t ad = desc0 + stage16, bd = ad + (uint32_t)a.ks * a16;
+                        const uint64_t sd = sdesc0 + (((uint32_t)sf.at * a.slot_bytes) >> 4);
+                        for (int kb = kb0; kb < kb1; ++kb, ad += a16, bd += b16) {
+                            const uint32_t q = (uint32_t)(kb % kXSuper);
+                            const uint32_t sfa = sf_col + 16u * (q & 1u), sfb = sfa + 4u;
+                            const uint64_t sda = sd + q * 32u;
+                            const uint64_t sdb = sd + 128u + ((q * a.tiled_b) >> 4);
+                            if (PAIR) {
+                                tmem_cp_scales_pair(sfa, sda);
+                                tmem_cp_scales_pair(sfb, sdb);
+                                if (n > 128u) tmem_cp_scales_pair(sfb + 4u, sdb + 32u);
+                            } else {
+                                tmem_cp_scales(sfa, sda);
+                                tmem_cp_scales(sfb, sdb);
+                                if (n > 128u) tmem_cp_scales(sfb + 4u, sdb + 32u);
+                            }
+#pragma unroll
+                            for (uint32_t k = 0; k < 4; ++k) {
+                                const uint32_t id = mx_idesc_at(idesc, 0, k);
+                                const uint32_t more = kb > 0 || k > 0 ? 1u : 0u;
+                                if (PAIR)
+                                    umma_mx_pair(d, ad + 2u * k, bd + 2u * k, id, sfa, sfb, more);
+                                else
+                                    umma_mx(d, ad + 2u * k, bd + 2u * k, id, sfa, sfb, more);
+                            }
+                        }
+                        if (PAIR) {
+                            umma_commit_pair(empty_bar(st.at));
+                            if (last) umma_commit_pair(free_bar(sf.at));
+                            if (kb1 == a.num_kb) umma_commit_pair(tfull_bar(acc.at));
+                        } else {
+                            umma_commit(empty_bar(st.at));
+                            if (last) umma_commit(free_bar(sf.at));
+                            if (kb1 == a.num_kb) umma_commit(tfull_bar(acc.at));
+                        }
+                    }
+                    st.next(S);
+                    if (last) sf.next(R);
                 }
-                st.next(S);
-                if (last) sf.next(R);
+                acc.next(2);
             }
-            acc.next(2);
+            if (!ok) *abort_v = 1;
+            // Every MMA and copy issued above has completed before the columns are freed.
+            if (leader) {
+                if (PAIR)
+                    umma_commit_pair(drain_bar);
+                else
+                    umma_commit(drain_bar);
+            }
+            mbar_wait(drain_bar, 0u, a.status);
+        }
+    } else if (warp == 2) {
+        const bool leader = elect_one();
+        Walk walk(a, off, parts, kCtas, rank);
+        Tile w;
+        Ring sf;
+        uint32_t filled = 0;
+        bool ok = true;
+        const int supers = (a.num_kb + kXSuper - 1) / kXSuper;
+        for (; ok && !*abort_v && walk.tile(w); walk.next()) {
+            const int wrow = w.e * a.N + w.f0;
+            for (int c = 0; c < supers; ++c) {
+                ok = mbar_wait(free_bar(sf.at), sf.pass ^ 1u, a.status);
+                if (!ok) break;
+                if (leader) {
+                    const uint32_t sl = base + a.sf + (uint32_t)sf.at * a.slot_bytes;
+                    const uint32_t bar = raw_bar(sf.at);
+                    mbar_arrive_expect_tx(bar, a.slot_tx);
+                    tma_load_2d(sl, &map_w0s, bar, 16 * c, wrow);
+                    if (GATE_UP)
+                        tma_load_2d(sl + (uint32_t)a.ft * 16u, &map_w1s, bar, 16 * c, wrow);
+                    tma_load_2d(sl + 2048u, &map_xs, bar, 16 * c, w.row0);
+                }
+                sf.next(R);
+                ++filled;
+            }
         }
         if (!ok) *abort_v = 1;
-        // Every MMA and copy issued above has completed before the columns are freed.
-        if (leader) umma_commit(drain_bar);
-        mbar_wait(drain_bar, 0u, a.status);
-    } else if (warp == 2 || warp == 3) {
-        Walk walk(a, off, parts);
+        for (uint32_t i = 0, n = min(filled, (uint32_t)R); i < n; ++i) {
+            sf.back(R);
+            if (!mbar_wait(raw_bar(sf.at), sf.pass, a.status)) break;
+        }
+    } else if (warp == 3) {
+        Walk walk(a, off, parts, kCtas, rank);
         Tile w;
         Ring sf;
         const int supers = (a.num_kb + kXSuper - 1) / kXSuper;
         bool ok = true;
-        // The row of a lane in a 32-row piece i of 128 rows, and its place in the 512-byte tile:
-        // a quarter-warp's 8 rows lie 32 rows from the next one's, so that the warp's 32 words
-        // fill 128 contiguous bytes.
-        const int row0 = (lane & 7) + 32 * (lane >> 3);
-        const int dst0 = (lane & 7) * 16 + (lane >> 3) * 4;
-        for (; ok && walk.tile(w); walk.next()) {
-            const int pb = w.n <= 128 ? 4 : 8;
+        const uint32_t lead_ready = PAIR ? cluster_map(ready_bar(0), 0) : ready_bar(0);
+        for (; ok && !*abort_v && walk.tile(w); walk.next()) {
             for (int c = 0; c < supers; ++c) {
-                ok = __all_sync(MOE_FULL_MASK,
-                                !*abort_v && mbar_wait(raw_bar(sf.at), sf.pass, a.status));
+                ok = __all_sync(MOE_FULL_MASK, mbar_wait(raw_bar(sf.at), sf.pass, a.status));
                 if (!ok) break;
                 uint8_t *sl = gbase + a.sf + (size_t)sf.at * a.slot_bytes;
-                // warp 2 turns the pieces 0, 2, .. and warp 3 the others
-                turn_scales(sl, sl + 2048 + a.raw_b, 512, warp - 2, 4, 128, row0, dst0);
-                turn_scales(sl + 2048, sl + 4096 + a.raw_b, (int)a.tiled_b, warp - 2, pb, a.cap,
-                            row0, dst0);
+                uint8_t *tiles = sl + 2048 + a.raw_b;
+                turn_scales(sl, tiles, 512u, lane);
+                turn_scales(sl + 2048, tiles + 2048, a.tiled_b, lane);
+                if (w.n > 128) turn_scales(sl + 4096, tiles + 2560, a.tiled_b, lane);
                 fence_async_shared();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(ready_bar(sf.at));
+                if (lane == 0) {
+                    if (PAIR)
+                        mbar_arrive_cluster(lead_ready + 8u * (uint32_t)sf.at);
+                    else
+                        mbar_arrive(ready_bar(sf.at));
+                }
                 sf.next(R);
             }
         }
         if (!ok) *abort_v = 1;
-    } else if (warp >= 4) {
-        // Two warps share a quarter of the TMEM lanes, half of a chunk's columns each.
+    } else {
+        // Two warps share a quarter of the TMEM lanes, half of a chunk's token columns each.
+        // gate_up: the 32 gate features of quarter q and the same up features, ft / 32 quarters
+        // on, are an MX block; the two warps that hold them meet in a staging buffer of their
+        // own.  down: a warp's 32 features are its own affair.
         const int q = warp & 3, half = (warp - 4) >> 2;
-        const int tid = (int)threadIdx.x - 128;
-        float *stg = reinterpret_cast<float *>(gbase + a.stg);
-        Walk walk(a, off, parts);
+        const int quarters = (GATE_UP ? 2 : 1) * a.ft / 32, up = a.ft / 32;
+        const bool works = q < quarters;
+        const int duo = GATE_UP ? q % up : q;  // block of 32 features
+        const int member = GATE_UP && q >= up ? 1 : 0;
+        const int bar_id = 2 + 2 * duo + half;
+        constexpr int kPitch = kXPitch[GATE_UP], kBuffer = kXBuffer[GATE_UP];
+        float *stg = reinterpret_cast<float *>(gbase + a.stg) +
+                     (2 * duo + half) * ((GATE_UP ? 2 : 1) * kBuffer);
+        Walk walk(a, off, parts, kCtas, rank);
         Tile w;
         Ring acc;
-        // 8-feature groups of a token: a thread keeps its group (8 or 16 of them a tile).
-        const int shift = a.ft == 128 ? 4 : a.ft == 64 ? 3 : 2;
-        const int grp = tid & ((1 << shift) - 1), tok0 = tid >> shift, tok_step = kXEpiThreads >> shift;
+        const int grp = lane & 3;  // 8 of the block's features
+        const int cover = a.f_tiles * kCtas * a.ft;  // features of all tiles, N or a little more
+        const uint32_t lead_tempty = PAIR ? cluster_map(tempty_bar(0), 0) : tempty_bar(0);
+        int buf = 0;
         for (; walk.tile(w); walk.next()) {
-            // Every epilogue thread goes by the same answer: they meet at the barriers below.
-            int ok = !*abort_v && mbar_wait(tfull_bar(acc.at), acc.pass, a.status);
+            // One thread polls; the others wait at the barrier that carries its answer.
+            int ok = threadIdx.x != 128 ||
+                     (!*abort_v && mbar_wait(tfull_bar(acc.at), acc.pass, a.status));
             asm volatile(
                 "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %0, 0;\n\t"
                 "barrier.red.and.pred q, 1, %1, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
@@ -434,42 +538,46 @@ __global__ void __launch_bounds__(kXThreads, 1)
                 break;
             }
             tc_fence_after();
-            const uint32_t trow = tmem_base + (uint32_t)(acc.at * a.acc_cols) +
-                                  ((uint32_t)(q * 32) << 16) + (uint32_t)(16 * half);
-            const int f = w.f0 + 8 * grp;
+            const uint32_t trow = tmem_base + (uint32_t)(acc.at * a.cap) +
+                                  ((uint32_t)(q * 32) << 16) + (uint32_t)(kXChunkHalf * half);
+            const int f = w.f0 + 32 * duo + 8 * grp;
             const bool real_f = f < a.N;
+            const int mine = w.n - kXChunkHalf * half;  // tokens from this half's first on
+            uint32_t v[kXChunkHalf];
+            if (works && mine > 0) tmem_ld16_nowait(trow, v);
             float b0[8], b1[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) b0[k] = b1[k] = 0.0f;
             if (real_f && a.bias0) load8(a.bias0 + (int64_t)w.e * a.N + f, b0);
             if (GATE_UP && real_f && a.bias1) load8(a.bias1 + (int64_t)w.e * a.N + f, b1);
-            for (int c0 = 0; c0 < w.n; c0 += kXChunk) {
-                uint32_t v[16];
-                tmem_ld16(trow + (uint32_t)c0, v);
-                if (c0 + kXChunk >= w.n) {  // the accumulator is free for the tile after next
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(tempty_bar(acc.at));
-                }
-                epi_sync();  // the last chunk's readers are done
+            for (int c0 = 0; works && c0 < mine; c0 += kXChunk, buf ^= 1) {
+                // gate_up: two buffers and one meeting a chunk: whoever is past the meeting of
+                // the chunk before has read the chunk before that.
+                float *sb = stg + (GATE_UP ? buf * kBuffer : 0);
+                tmem_wait_ld();
+                if (!GATE_UP) __syncwarp();
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    stg[(16 * half + i) * kXPitch + 32 * q + lane] = __uint_as_float(v[i]);
-                epi_sync();
-                const int left = w.n - c0;
-                // whole warps go on while any of their tokens is there (the block's shuffles)
-                for (int tok = tok0; tok < kXChunk; tok += tok_step) {
-                    const bool there = tok < left;
-                    if (!__any_sync(MOE_FULL_MASK, there)) break;
-                    const int64_t row = (int64_t)w.row0 + c0 + tok;
-                    const float *src = stg + tok * kXPitch + 8 * grp;
+                for (int i = 0; i < kXChunkHalf; ++i)
+                    sb[i * kPitch + 32 * member + lane] = __uint_as_float(v[i]);
+                if (c0 + kXChunk < mine) tmem_ld16_nowait(trow + (uint32_t)(c0 + kXChunk), v);
+                if (GATE_UP)
+                    asm volatile("bar.sync %0, 64;" ::"r"(bar_id) : "memory");
+                else
+                    __syncwarp();
+                // 16 tokens, four lanes each: 8 a warp (gate_up) or both eights (down)
+#pragma unroll
+                for (int t8 = 0; t8 < (GATE_UP ? 1 : 2); ++t8) {
+                    const int tok = 8 * (GATE_UP ? member : t8) + (lane >> 2);
+                    const bool there = c0 + tok < mine;
+                    const int64_t row = (int64_t)w.row0 + kXChunkHalf * half + c0 + tok;
+                    const float *src = sb + tok * kPitch + 8 * grp;
                     float o[8];
                     load8(src, o);
 #pragma unroll
                     for (int k = 0; k < 8; ++k) o[k] += b0[k];
                     if (GATE_UP) {
                         float u[8];
-                        load8(src + a.ft, u);
+                        load8(src + 32, u);
 #pragma unroll
                         for (int k = 0; k < 8; ++k) u[k] += b1[k];
                         activate8(o, u, a.act);
@@ -482,15 +590,23 @@ __global__ void __launch_bounds__(kXThreads, 1)
                     }
                 }
             }
+            // This warp's reads are done: the accumulator is free for the tile after next.
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (PAIR)
+                    mbar_arrive_cluster(lead_tempty + 8u * (uint32_t)acc.at);
+                else
+                    mbar_arrive(tempty_bar(acc.at));
+            }
             // The last feature tile's tokens get what is left of their rows' padding.
-            if (GATE_UP && w.f0 + a.ft >= a.N) {
-                for (int i = tid; i < w.n; i += kXEpiThreads) {
+            if (GATE_UP && w.f0 + a.ft == cover) {
+                for (int i = (int)threadIdx.x - 128; i < w.n; i += kXEpiThreads) {
                     const int64_t row = (int64_t)w.row0 + i;
                     uint8_t *qrow = a.hq + row * a.h_row, *srow = a.hs + row * a.h_scale;
-                    const int64_t from = a.h_fmt == MOE_MX_E4M3 ? w.f0 + a.ft : (w.f0 + a.ft) / 2;
-                    for (int64_t k = from; k < a.h_row; k += 16)
+                    for (int64_t k = a.h_fmt == MOE_MX_E4M3 ? cover : cover / 2; k < a.h_row; k += 16)
                         *reinterpret_cast<uint4 *>(qrow + k) = make_uint4(0u, 0u, 0u, 0u);
-                    for (int64_t k = (w.f0 + a.ft) / kMxBlock; k < a.h_scale; ++k) srow[k] = 0;
+                    for (int64_t k = cover / kMxBlock; k < a.h_scale; ++k) srow[k] = 0;
                 }
             }
             acc.next(2);
@@ -498,46 +614,44 @@ __global__ void __launch_bounds__(kXThreads, 1)
     }
 
     tc_fence_before();
-    __syncthreads();
+    if (PAIR)
+        cluster_sync();  // no CTA leaves while the other may use its memory or barriers
+    else
+        __syncthreads();
     if (warp == 2) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
-                     "r"(a.tmem_cols)
-                     : "memory");
+        if (PAIR)
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
+                         "r"(a.tmem_cols)
+                         : "memory");
+        else
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
+                         "r"(a.tmem_cols)
+                         : "memory");
     }
 }
 
-bool operand_map(CUtensorMap *m, const void *q, int64_t rows, int32_t K, int32_t format, int box) {
-    return format == MOE_MX_E4M3 ? make_byte_map(m, q, rows, mx_padded(K), box, 128)
-                                 : make_nibble_map(m, q, rows, mx_padded(K), box);
-}
-
-template <bool GATE_UP>
+template <bool GATE_UP, bool PAIR>
 moe_status launch_expert_mx(const uint8_t *xq, const uint8_t *xs, int32_t x_fmt, const uint8_t *w0,
                             const uint8_t *w0s, const uint8_t *w1, const uint8_t *w1s,
                             int32_t w_fmt, int32_t K, MxFfnArgs a, moe_stream_t stream) {
-    // Token columns of a tile: enough for four times an expert's share of the rows, so that few
-    // experts need a second part (which reads the weights again); a narrow tile leaves shared
-    // memory to more weight stages.
-    const int64_t share = 4 * ((a.rows + a.E - 1) / a.E);
-    a.cap = share <= 32 ? 32 : share <= 64 ? 64 : share <= 128 ? 128 : 224;
-    a.box = a.cap / 2;  // one or two loads a stage
-    a.acc_cols = a.cap;
-    a.ft = GATE_UP ? 64 : 128;
-    a.f_tiles = (a.N + a.ft - 1) / a.ft;
+    constexpr int kCtas = PAIR ? 2 : 1;
+    const bool w4 = w_fmt == MOE_MX_E2M1, x4 = x_fmt == MOE_MX_E2M1;
+    a.f_tiles = (a.N + kCtas * a.ft - 1) / (kCtas * a.ft);
     a.num_kb = mx_padded(K) / kXBK;
-    const int a_rows = (GATE_UP ? 2 : 1) * a.ft;
+    const int a_rows = (GATE_UP ? 2 : 1) * a.ft, b_rows = a.cap / kCtas;
     a.a_bytes = (uint32_t)a_rows * 128u;
-    a.stage_bytes = a.a_bytes + (uint32_t)a.cap * 128u;
-    a.raw_b = (uint32_t)a.cap * 16u;
+    a.b_bytes = (uint32_t)b_rows * 128u;
+    a.stage_bytes = (uint32_t)a.ks * (a.a_bytes + a.b_bytes);
+    a.stage_tx = (uint32_t)(kCtas * a.ks) *
+                 ((w4 ? a.a_bytes / 2 : a.a_bytes) + (x4 ? a.b_bytes / 2 : a.b_bytes));
+    a.slot_tx = (uint32_t)(a_rows + a.cap) * 16u;
+    a.raw_b = a.cap > 128 ? 4096u : 2048u;
     a.tiled_b = a.cap > 128 ? 1024u : 512u;
     a.slot_bytes = 2048u + a.raw_b + 2048u + 4u * a.tiled_b;
-    a.slots = 2;
-    a.w_count = w_fmt == MOE_MX_E4M3 ? 128u : 64u;
-    a.x_count = x_fmt == MOE_MX_E4M3 ? 128u : 64u;
-    a.idesc = mx_idesc(w_fmt == MOE_MX_E4M3 ? 0u : 5u, x_fmt == MOE_MX_E4M3 ? 0u : 5u, 128u);
+    a.idesc = mx_idesc(w4 ? 5u : 0u, x4 ? 5u : 0u, 128u * kCtas);
     int cols = 32;
-    while (cols < 2 * a.acc_cols + 32) cols *= 2;
+    while (cols < 2 * a.cap + 32) cols *= 2;
     a.tmem_cols = cols;
     int dev = 0, max_smem = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -546,16 +660,16 @@ moe_status launch_expert_mx(const uint8_t *xq, const uint8_t *xs, int32_t x_fmt,
         cudaGetLastError();
         return MOE_ERR_CUDA;
     }
-    const uint32_t stg = kXChunk * kXPitch * 4, bars = 512;
+    const uint32_t stg = kXStageBytes[GATE_UP], bars = 512;
     const uint32_t tables = ((uint32_t)(2 * (a.E + 1)) * 4u + 15u) / 16u * 16u;
-    // alignment slack, static shared memory
+    // alignment slack, static shared memory; MMAs read 128 weight rows where a tile has fewer:
+    // what lies behind the stages is large enough for that
     const int64_t rest = (int64_t)max_smem - 1024 - 64 - stg - bars - tables -
                          (int64_t)a.slots * a.slot_bytes;
     int64_t stages = rest / a.stage_bytes;
-    if (stages > 12) stages = 12;
+    if (stages > kXMaxStages) stages = kXMaxStages;
     if (stages < 2) return MOE_ERR_UNSUPPORTED;
     a.stages = (int)stages;
-    a.ring = 0;
     a.sf = (uint32_t)a.stages * a.stage_bytes;
     a.stg = a.sf + (uint32_t)a.slots * a.slot_bytes;
     a.bars = a.stg + stg;
@@ -563,15 +677,19 @@ moe_status launch_expert_mx(const uint8_t *xq, const uint8_t *xs, int32_t x_fmt,
     const size_t smem = 1024 + (size_t)a.tables + tables;
     CUtensorMap mw0, mw1, mw0s, mw1s, mx, mxs;
     const int64_t wrows = (int64_t)a.E * a.N;
-    const int64_t sp = mx_scale_bytes(K);
-    if (!operand_map(&mw0, w0, wrows, K, w_fmt, a.ft) ||
-        !operand_map(&mw1, GATE_UP ? w1 : w0, wrows, K, w_fmt, a.ft) ||
-        !make_byte_map(&mw0s, w0s, wrows, sp, a.ft, 16) ||
-        !make_byte_map(&mw1s, GATE_UP ? w1s : w0s, wrows, sp, a.ft, 16) ||
-        !operand_map(&mx, xq, a.rows, K, x_fmt, a.box) ||
-        !make_byte_map(&mxs, xs, a.rows, sp, a.box, 16))
+    const int64_t Kp = mx_padded(K), sp = mx_scale_bytes(K);
+    const int w_k = GATE_UP ? 1 : a.ks;  // gate and up tiles alternate: one K block a load
+    if (!make_mx_map(&mw0, w0, wrows, Kp, w4, a.ft, w_k) ||
+        !make_byte_map(&mw0s, w0s, wrows, sp, a.ft) ||
+        !make_mx_map(&mx, xq, a.rows, Kp, x4, b_rows, a.ks) ||
+        !make_byte_map(&mxs, xs, a.rows, sp, a.cap))
         return MOE_ERR_CUDA;
-    if (cudaFuncSetAttribute(expert_mx_kernel<GATE_UP>,
+    mw1 = mw0;
+    mw1s = mw0s;
+    if (GATE_UP && (!make_mx_map(&mw1, w1, wrows, Kp, w4, a.ft, w_k) ||
+                    !make_byte_map(&mw1s, w1s, wrows, sp, a.ft)))
+        return MOE_ERR_CUDA;
+    if (cudaFuncSetAttribute(expert_mx_kernel<GATE_UP, PAIR>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
         cudaSuccess) {
         cudaGetLastError();
@@ -579,14 +697,46 @@ moe_status launch_expert_mx(const uint8_t *xq, const uint8_t *xs, int32_t x_fmt,
     }
     // Never more CTAs than the most tiles these rows can make.
     const int64_t parts = a.rows / a.cap + (a.rows < a.E ? a.rows : a.E);
-    const int64_t most = parts * a.f_tiles;
-    const int64_t grid = most < sm_count() ? most : sm_count();
-    if (launch_pdl(expert_mx_kernel<GATE_UP>, dim3((unsigned)grid), dim3(kXThreads), smem,
-                   as_cuda(stream), mw0, mw1, mw0s, mw1s, mx, mxs, a) != cudaSuccess) {
+    const int64_t most = parts * a.f_tiles, slots = sm_count() / kCtas;
+    const unsigned grid = (unsigned)(kCtas * (most < slots ? most : slots));
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = pdl_config(dim3(grid), dim3(kXThreads), smem, as_cuda(stream), attr);
+    if (PAIR) {
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = 2;
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = 1;
+        cfg.numAttrs = 2;
+    }
+    if (cudaLaunchKernelEx(&cfg, expert_mx_kernel<GATE_UP, PAIR>, mw0, mw1, mw0s, mw1s, mx, mxs,
+                           a) != cudaSuccess) {
         cudaGetLastError();
         return MOE_ERR_CUDA;
     }
     return launch_status();
+}
+
+// Tile shape by the rows an expert has on average.  With few, the weights' bytes are the time:
+// narrow token tiles leave shared memory to weight stages of two K blocks.  With many, the
+// products are: pairs of CTAs, each holding half of the tokens.
+template <bool GATE_UP>
+moe_status run_expert_mx(const uint8_t *xq, const uint8_t *xs, int32_t x_fmt, const uint8_t *w0,
+                         const uint8_t *w0s, const uint8_t *w1, const uint8_t *w1s, int32_t w_fmt,
+                         int32_t K, MxFfnArgs a, moe_stream_t stream) {
+    const int64_t share = (a.rows + a.E - 1) / a.E;
+    a.ft = GATE_UP ? 64 : 128;
+    if (share <= 32) {
+        // four times the average: few experts need a second part, which reads the weights again
+        a.cap = share <= 4 ? 16 : share <= 8 ? 32 : share <= 16 ? 64 : 128;
+        a.ks = a.cap <= 64 ? 2 : 1;
+        a.slots = 4;
+        return launch_expert_mx<GATE_UP, false>(xq, xs, x_fmt, w0, w0s, w1, w1s, w_fmt, K, a,
+                                                stream);
+    }
+    a.cap = share <= 64 ? 128 : 224;
+    a.ks = 1;
+    a.slots = 3;
+    return launch_expert_mx<GATE_UP, true>(xq, xs, x_fmt, w0, w0s, w1, w1s, w_fmt, K, a, stream);
 }
 
 moe_status check_ffn_mx(const void *x, const void *xs, int32_t x_fmt, int32_t w_fmt,
@@ -635,7 +785,7 @@ extern "C" moe_status moe_expert_gate_up_mx(const uint8_t *xq, const uint8_t *xs
     a.E = E;
     a.N = F;
     a.act = act;
-    return launch_expert_mx<true>(xq, xs, x_format, w1, w1_scales, w3, w3_scales, w_format, d, a,
+    return run_expert_mx<true>(xq, xs, x_format, w1, w1_scales, w3, w3_scales, w_format, d, a,
                                   stream);
 }
 
@@ -659,6 +809,6 @@ extern "C" moe_status moe_expert_down_mx(const uint8_t *h, const uint8_t *h_scal
     a.E = E;
     a.N = d;
     a.act = MOE_ACT_SWIGLU;
-    return launch_expert_mx<false>(h, h_scales, h_format, w2, w2_scales, nullptr, nullptr, w_format,
+    return run_expert_mx<false>(h, h_scales, h_format, w2, w2_scales, nullptr, nullptr, w_format,
                                    F, a, stream);
 }

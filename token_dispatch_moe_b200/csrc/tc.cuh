@@ -239,6 +239,20 @@ __device__ __forceinline__ void umma_mx(uint32_t tmem_d, uint64_t adesc, uint64_
         : "memory");
 }
 
+// ... of a CTA pair: 256 rows of A, B split between the CTAs by rows, and in each CTA's TMEM
+// the scales of its own 128 rows of A and of all N rows of B.
+__device__ __forceinline__ void umma_mx_pair(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
+                                             uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                             uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X"
+        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(tmem_d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
 // Descriptor of 512 bytes of scales (32 rows of 16 bytes, laid end to end): no
 // swizzle, 8 rows are 128 contiguous bytes.
 __device__ __forceinline__ uint64_t scales_desc(uint32_t saddr) {
@@ -253,6 +267,35 @@ __device__ __forceinline__ uint64_t scales_desc(uint32_t saddr) {
 __device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t desc) {
     asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
                  : "memory");
+}
+
+// ... in both CTAs of a pair, each from its own shared memory at this offset.
+__device__ __forceinline__ void tmem_cp_scales_pair(uint32_t taddr, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+                 : "memory");
+}
+
+// Arrival on an mbarrier of either CTA of the pair (bar: shared::cluster address).
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar,
+                                            int x, int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+// ... whose completion counts on an mbarrier of either CTA of the pair.  No multicast.
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap *map, uint32_t bar,
+                                                 int x, int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
 }
 
 // True in one lane of the (converged) warp.
@@ -304,37 +347,37 @@ inline bool make_map(CUtensorMap *m, const void *ptr, int64_t rows, int64_t cols
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// 2-D tensor of bytes [rows][pitch], box = box_rows x box_bytes, no swizzle or (box of 128
-// bytes) the 128-byte one.
+// 2-D tensor of bytes [rows][pitch], box = box_rows x 16 bytes, no swizzle.
 inline bool make_byte_map(CUtensorMap *m, const void *ptr, int64_t rows, int64_t pitch,
-                          int box_rows, int box_bytes) {
+                          int box_rows) {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return false;
     cuuint64_t dims[2] = {(cuuint64_t)pitch, (cuuint64_t)rows};
     cuuint64_t strides[1] = {(cuuint64_t)pitch};
-    cuuint32_t box[2] = {(cuuint32_t)box_bytes, (cuuint32_t)box_rows};
+    cuuint32_t box[2] = {16u, (cuuint32_t)box_rows};
     cuuint32_t estr[2] = {1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(ptr), dims, strides, box,
-               estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// 2-D tensor of packed 4-bit values [rows][cols] (cols a multiple of 128, 32-byte aligned),
-// box = box_rows x 128 values, widened to 8-bit containers in shared memory (16 values: 8
-// packed bytes and 8 unused), 128-byte swizzle.
-inline bool make_nibble_map(CUtensorMap *m, const void *ptr, int64_t rows, int64_t cols,
-                            int box_rows) {
+// Element rows [rows][cols] of an MX operand (cols a multiple of 128) as a 3-D tensor
+// [cols / 128][rows][128], box = box_k x box_rows x 128, 128-byte swizzle: box_k tiles of
+// box_rows rows in one load.  e4m3: bytes.  e2m1: packed in memory (32-byte aligned), widened
+// to 8-bit containers in shared memory (16 values: 8 packed bytes and 8 unused).
+inline bool make_mx_map(CUtensorMap *m, const void *ptr, int64_t rows, int64_t cols, bool packed,
+                        int box_rows, int box_k) {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return false;
-    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)cols / 2};
-    cuuint32_t box[2] = {128u, (cuuint32_t)box_rows};
-    cuuint32_t estr[2] = {1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 2, const_cast<void *>(ptr), dims, strides,
-               box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    const cuuint64_t pitch = (cuuint64_t)(packed ? cols / 2 : cols);
+    cuuint64_t dims[3] = {128u, (cuuint64_t)rows, (cuuint64_t)cols / 128};
+    cuuint64_t strides[2] = {pitch, packed ? 64u : 128u};
+    cuuint32_t box[3] = {128u, (cuuint32_t)box_rows, (cuuint32_t)box_k};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, packed ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
+               const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
