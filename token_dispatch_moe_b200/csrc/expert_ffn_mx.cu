@@ -68,10 +68,9 @@ struct MxFfnArgs {
     int ft;                  // features of a CTA's tile
     int f_tiles;             // tiles (of a CTA or a pair) that cover the features
     int cap;                 // most tokens of a tile; also the columns of an accumulator
-    int ks;                  // 128-value K blocks of a stage
     int num_kb, stages, slots, tmem_cols, act, h_fmt;
     uint32_t a_bytes, b_bytes;     // a K block's weight and token tile in shared memory
-    uint32_t stage_bytes;          // ks of both
+    uint32_t stage_bytes;          // KS of both
     uint32_t stage_tx, slot_tx;    // bytes their barriers count: 4-bit values packed
     uint32_t raw_b, tiled_b, slot_bytes, idesc;
     uint32_t sf, stg, bars, tables;  // offsets in shared memory (the stages come first)
@@ -187,6 +186,24 @@ struct Walk {
     }
 };
 
+// A K block's tile of an operand's rows.
+template <bool PAIR>
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap *map, uint32_t bar,
+                                          int row, int kb) {
+    if (PAIR)
+        tma_load_3d_pair(dst, map, bar, 0, row, kb);
+    else
+        tma_load_3d(dst, map, bar, 0, row, kb);
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void commit(uint32_t bar) {
+    if (PAIR)
+        umma_commit_pair(bar);
+    else
+        umma_commit(bar);
+}
+
 // A place in a ring of `size` buffers and the parity of the pass over it.
 struct Ring {
     int at = 0;
@@ -205,7 +222,7 @@ struct Ring {
     }
 };
 
-template <bool GATE_UP, bool PAIR>
+template <bool GATE_UP, bool PAIR, int KS>
 __global__ void __launch_bounds__(kXThreads, 1)
     expert_mx_kernel(const __grid_constant__ CUtensorMap map_w0,
                      const __grid_constant__ CUtensorMap map_w1,
@@ -304,175 +321,149 @@ __global__ void __launch_bounds__(kXThreads, 1)
     volatile int *abort_v = &abort_s;
     griddep_launch_dependents();
 
-    // Warps 0 to 3 run their loops whole, so that addresses and descriptors are uniform over
-    // the warp; one elected lane issues.
+    // The producers and the MMA issuer are one thread each, and their loops are unrolled over
+    // the K blocks that a load of scales covers: what bounds them is the length of the chain
+    // of instructions between two issues.
     if (warp == 0) {
-        const bool leader = elect_one();
-        Walk walk(a, off, parts, kCtas, rank);
-        Tile w;
-        Ring st;
-        uint32_t filled = 0;
-        bool ok = true;
-        const uint32_t lead_full = PAIR ? cluster_map(full_bar(0), 0) : full_bar(0);
-        for (; ok && !*abort_v && walk.tile(w); walk.next()) {
-            const int wrow = w.e * a.N + w.f0;
-            // a pair's tokens in multiples of 16: each CTA holds one half's rows
-            const int xrow = w.row0 + (PAIR ? rank * (((w.n + 15) & ~15) >> 1) : 0);
-            for (int kb = 0; kb < a.num_kb; kb += a.ks) {
-                ok = mbar_wait(empty_bar(st.at), st.pass ^ 1u, a.status);
-                if (!ok) break;
-                if (leader) {
+        if (elect_one()) {
+            Walk walk(a, off, parts, kCtas, rank);
+            Tile w;
+            Ring st;
+            uint32_t filled = 0;
+            bool ok = true;
+            const uint32_t lead_full = PAIR ? cluster_map(full_bar(0), 0) : full_bar(0);
+            const uint32_t up = (uint32_t)a.ft * 128u;
+            for (; ok && !*abort_v && walk.tile(w); walk.next()) {
+                const int wrow = w.e * a.N + w.f0;
+                // a pair's tokens in multiples of 16: each CTA holds one half's rows
+                const int xrow = w.row0 + (PAIR ? rank * (((w.n + 15) & ~15) >> 1) : 0);
+                for (int kb = 0; kb < a.num_kb; kb += KS) {
+                    ok = mbar_wait(empty_bar(st.at), st.pass ^ 1u, a.status);
+                    if (!ok) break;
                     uint32_t dst = base + (uint32_t)st.at * a.stage_bytes;
                     const uint32_t bar = lead_full + 8u * (uint32_t)st.at;
                     if (rank == 0) mbar_arrive_expect_tx(full_bar(st.at), a.stage_tx);
                     // K blocks behind the last are filled with zeros (and not multiplied)
                     if (GATE_UP) {
-                        for (int i = 0; i < a.ks; ++i) {
-                            if (PAIR) {
-                                tma_load_3d_pair(dst, &map_w0, bar, 0, wrow, kb + i);
-                                tma_load_3d_pair(dst + (uint32_t)a.ft * 128u, &map_w1, bar, 0, wrow,
-                                                 kb + i);
-                            } else {
-                                tma_load_3d(dst, &map_w0, bar, 0, wrow, kb + i);
-                                tma_load_3d(dst + (uint32_t)a.ft * 128u, &map_w1, bar, 0, wrow,
-                                            kb + i);
-                            }
+#pragma unroll
+                        for (int i = 0; i < KS; ++i) {
+                            load_tile<PAIR>(dst, &map_w0, bar, wrow, kb + i);
+                            load_tile<PAIR>(dst + up, &map_w1, bar, wrow, kb + i);
                             dst += a.a_bytes;
                         }
                     } else {
-                        if (PAIR)
-                            tma_load_3d_pair(dst, &map_w0, bar, 0, wrow, kb);
-                        else
-                            tma_load_3d(dst, &map_w0, bar, 0, wrow, kb);
-                        dst += (uint32_t)a.ks * a.a_bytes;
+                        load_tile<PAIR>(dst, &map_w0, bar, wrow, kb);
+                        dst += (uint32_t)KS * a.a_bytes;
                     }
-                    if (PAIR)
-                        tma_load_3d_pair(dst, &map_x, bar, 0, xrow, kb);
-                    else
-                        tma_load_3d(dst, &map_x, bar, 0, xrow, kb);
+                    load_tile<PAIR>(dst, &map_x, bar, xrow, kb);
+                    st.next(S);
+                    ++filled;
                 }
-                st.next(S);
-                ++filled;
+            }
+            if (!ok) *abort_v = 1;
+            // Drain (the leader's barriers count both CTAs' bytes): the last loads into every
+            // stage have landed before the CTAs exit.
+            for (uint32_t i = 0, n = rank == 0 ? min(filled, (uint32_t)S) : 0u; i < n; ++i) {
+                st.back(S);
+                if (!mbar_wait(full_bar(st.at), st.pass, a.status)) break;
             }
         }
-        if (!ok) *abort_v = 1;
-        // Drain (the leader's barriers count both CTAs' bytes): the last loads into every stage
-        // have landed before the CTAs exit.
-        for (uint32_t i = 0, n = rank == 0 ? min(filled, (uint32_t)S) : 0u; i < n; ++i) {
-            st.back(S);
-            if (!mbar_wait(full_bar(st.at), st.pass, a.status)) break;
-        }
     } else if (warp == 1) {
-        if (rank == 0) {
-            const bool leader = elect_one();
+        if (rank == 0 && elect_one()) {
             Walk walk(a, off, parts, kCtas, rank);
             Tile w;
             Ring st, sf, acc;
             bool ok = true;
             const uint32_t sf_col = tmem_base + 2u * (uint32_t)a.cap;
-            // descriptors: only the start address differs
-            const uint64_t desc0 = sw128_desc(base), sdesc0 = scales_desc(base + a.sf + 2048u + a.raw_b);
+            // descriptors: only the start address, in the low word, differs
+            const uint64_t d0 = sw128_desc(base), s0 = scales_desc(base + a.sf + 2048u + a.raw_b);
+            const uint32_t d_hi = (uint32_t)(d0 >> 32), s_hi = (uint32_t)(s0 >> 32);
             const uint32_t a16 = a.a_bytes >> 4, b16 = a.b_bytes >> 4;
+            const uint32_t stage16 = a.stage_bytes >> 4, slot16 = a.slot_bytes >> 4;
+            const uint32_t tiled16 = a.tiled_b >> 4;
+            uint32_t d_lo = (uint32_t)d0, s_lo = (uint32_t)s0;  // of the ring places in use
             for (; ok && !*abort_v && walk.tile(w); walk.next()) {
                 const uint32_t n = PAIR ? (uint32_t)(w.n + 15) & ~15u : (uint32_t)(w.n + 7) & ~7u;
-                const uint32_t idesc = mx_idesc_at(a.idesc, n, 0);
+                uint32_t idesc[4];
+#pragma unroll
+                for (uint32_t k = 0; k < 4; ++k) idesc[k] = mx_idesc_at(a.idesc, n, k);
+                const bool wide = n > 128u;
                 ok = mbar_wait(tempty_bar(acc.at), acc.pass ^ 1u, a.status);
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t d = tmem_base + (uint32_t)(acc.at * a.cap);
-                for (int kb0 = 0; kb0 < a.num_kb; kb0 += a.ks) {
-                    if (kb0 % kXSuper == 0) {
-                        ok = mbar_wait(ready_bar(sf.at), sf.pass, a.status);
-                        if (!ok) break;
-                    }
-                    ok = mbar_wait(full_bar(st.at), st.pass, a.status);
+                uint32_t more = 0;
+                for (int left = a.num_kb; left > 0; left -= kXSuper) {
+                    ok = mbar_wait(ready_bar(sf.at), sf.pass, a.status);
                     if (!ok) break;
-                    tc_fence_after();
-                    const int kb1 = min(kb0 + a.ks, a.num_kb);
-                    const bool last = kb1 % kXSuper == 0 || kb1 == a.num_kb;
-                    if (leader) {
-                        const uint32_t stage16 = ((uint32_t)st.at * a.stage_bytes) >> 4;
-                        uint64_t ad = desc0 + stage16, bd = ad + (uint32_t)a.ks * a16;
-                        const uint64_t sd = sdesc0 + (((uint32_t)sf.at * a.slot_bytes) >> 4);
-                        for (int kb = kb0; kb < kb1; ++kb, ad += a16, bd += b16) {
-                            const uint32_t q = (uint32_t)(kb % kXSuper);
-                            const uint32_t sfa = sf_col + 16u * (q & 1u), sfb = sfa + 4u;
-                            const uint64_t sda = sd + q * 32u;
-                            const uint64_t sdb = sd + 128u + ((q * a.tiled_b) >> 4);
-                            if (PAIR) {
-                                tmem_cp_scales_pair(sfa, sda);
-                                tmem_cp_scales_pair(sfb, sdb);
-                                if (n > 128u) tmem_cp_scales_pair(sfb + 4u, sdb + 32u);
-                            } else {
-                                tmem_cp_scales(sfa, sda);
-                                tmem_cp_scales(sfb, sdb);
-                                if (n > 128u) tmem_cp_scales(sfb + 4u, sdb + 32u);
-                            }
 #pragma unroll
-                            for (uint32_t k = 0; k < 4; ++k) {
-                                const uint32_t id = mx_idesc_at(idesc, 0, k);
-                                const uint32_t more = kb > 0 || k > 0 ? 1u : 0u;
-                                if (PAIR)
-                                    umma_mx_pair(d, ad + 2u * k, bd + 2u * k, id, sfa, sfb, more);
-                                else
-                                    umma_mx(d, ad + 2u * k, bd + 2u * k, id, sfa, sfb, more);
-                            }
+                    for (int q = 0; q < kXSuper; ++q) {
+                        if (q >= left) break;
+                        if (q % KS == 0) {
+                            ok = mbar_wait(full_bar(st.at), st.pass, a.status);
+                            if (!ok) break;
+                            tc_fence_after();
                         }
-                        if (PAIR) {
-                            umma_commit_pair(empty_bar(st.at));
-                            if (last) umma_commit_pair(free_bar(sf.at));
-                            if (kb1 == a.num_kb) umma_commit_pair(tfull_bar(acc.at));
-                        } else {
-                            umma_commit(empty_bar(st.at));
-                            if (last) umma_commit(free_bar(sf.at));
-                            if (kb1 == a.num_kb) umma_commit(tfull_bar(acc.at));
+                        const uint32_t sfa = sf_col + 16u * (q & 1), sfb = sfa + 4u;
+                        const uint32_t sb = s_lo + 128u + (uint32_t)q * tiled16;
+                        tmem_cp_scales<PAIR>(sfa, s_lo + 32u * q, s_hi);
+                        tmem_cp_scales<PAIR>(sfb, sb, s_hi);
+                        if (wide) tmem_cp_scales<PAIR>(sfb + 4u, sb + 32u, s_hi);
+                        const uint32_t a_lo = d_lo + (uint32_t)(q % KS) * a16;
+                        const uint32_t b_lo = d_lo + (uint32_t)KS * a16 + (uint32_t)(q % KS) * b16;
+#pragma unroll
+                        for (uint32_t k = 0; k < 4; ++k) {
+                            umma_mx<PAIR>(d, a_lo + 2u * k, b_lo + 2u * k, d_hi, idesc[k], sfa, sfb,
+                                          more);
+                            more = 1u;
+                        }
+                        if (q % KS == KS - 1 || q + 1 == left) {
+                            commit<PAIR>(empty_bar(st.at));
+                            st.next(S);
+                            d_lo = st.at == 0 ? (uint32_t)d0 : d_lo + stage16;
                         }
                     }
-                    st.next(S);
-                    if (last) sf.next(R);
+                    if (!ok) break;
+                    commit<PAIR>(free_bar(sf.at));
+                    sf.next(R);
+                    s_lo = sf.at == 0 ? (uint32_t)s0 : s_lo + slot16;
                 }
+                if (!ok) break;
+                commit<PAIR>(tfull_bar(acc.at));
                 acc.next(2);
             }
             if (!ok) *abort_v = 1;
             // Every MMA and copy issued above has completed before the columns are freed.
-            if (leader) {
-                if (PAIR)
-                    umma_commit_pair(drain_bar);
-                else
-                    umma_commit(drain_bar);
-            }
+            commit<PAIR>(drain_bar);
             mbar_wait(drain_bar, 0u, a.status);
         }
     } else if (warp == 2) {
-        const bool leader = elect_one();
-        Walk walk(a, off, parts, kCtas, rank);
-        Tile w;
-        Ring sf;
-        uint32_t filled = 0;
-        bool ok = true;
-        const int supers = (a.num_kb + kXSuper - 1) / kXSuper;
-        for (; ok && !*abort_v && walk.tile(w); walk.next()) {
-            const int wrow = w.e * a.N + w.f0;
-            for (int c = 0; c < supers; ++c) {
-                ok = mbar_wait(free_bar(sf.at), sf.pass ^ 1u, a.status);
-                if (!ok) break;
-                if (leader) {
+        if (elect_one()) {
+            Walk walk(a, off, parts, kCtas, rank);
+            Tile w;
+            Ring sf;
+            uint32_t filled = 0;
+            bool ok = true;
+            for (; ok && !*abort_v && walk.tile(w); walk.next()) {
+                const int wrow = w.e * a.N + w.f0;
+                for (int c = 0; c < a.num_kb; c += kXSuper) {
+                    ok = mbar_wait(free_bar(sf.at), sf.pass ^ 1u, a.status);
+                    if (!ok) break;
                     const uint32_t sl = base + a.sf + (uint32_t)sf.at * a.slot_bytes;
                     const uint32_t bar = raw_bar(sf.at);
                     mbar_arrive_expect_tx(bar, a.slot_tx);
-                    tma_load_2d(sl, &map_w0s, bar, 16 * c, wrow);
-                    if (GATE_UP)
-                        tma_load_2d(sl + (uint32_t)a.ft * 16u, &map_w1s, bar, 16 * c, wrow);
-                    tma_load_2d(sl + 2048u, &map_xs, bar, 16 * c, w.row0);
+                    tma_load_2d(sl, &map_w0s, bar, 4 * c, wrow);
+                    if (GATE_UP) tma_load_2d(sl + (uint32_t)a.ft * 16u, &map_w1s, bar, 4 * c, wrow);
+                    tma_load_2d(sl + 2048u, &map_xs, bar, 4 * c, w.row0);
+                    sf.next(R);
+                    ++filled;
                 }
-                sf.next(R);
-                ++filled;
             }
-        }
-        if (!ok) *abort_v = 1;
-        for (uint32_t i = 0, n = min(filled, (uint32_t)R); i < n; ++i) {
-            sf.back(R);
-            if (!mbar_wait(raw_bar(sf.at), sf.pass, a.status)) break;
+            if (!ok) *abort_v = 1;
+            for (uint32_t i = 0, n = min(filled, (uint32_t)R); i < n; ++i) {
+                sf.back(R);
+                if (!mbar_wait(raw_bar(sf.at), sf.pass, a.status)) break;
+            }
         }
     } else if (warp == 3) {
         Walk walk(a, off, parts, kCtas, rank);
@@ -631,7 +622,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
     }
 }
 
-template <bool GATE_UP, bool PAIR>
+template <bool GATE_UP, bool PAIR, int KS>
 moe_status launch_expert_mx(const uint8_t *xq, const uint8_t *xs, int32_t x_fmt, const uint8_t *w0,
                             const uint8_t *w0s, const uint8_t *w1, const uint8_t *w1s,
                             int32_t w_fmt, int32_t K, MxFfnArgs a, moe_stream_t stream) {
@@ -642,8 +633,8 @@ moe_status launch_expert_mx(const uint8_t *xq, const uint8_t *xs, int32_t x_fmt,
     const int a_rows = (GATE_UP ? 2 : 1) * a.ft, b_rows = a.cap / kCtas;
     a.a_bytes = (uint32_t)a_rows * 128u;
     a.b_bytes = (uint32_t)b_rows * 128u;
-    a.stage_bytes = (uint32_t)a.ks * (a.a_bytes + a.b_bytes);
-    a.stage_tx = (uint32_t)(kCtas * a.ks) *
+    a.stage_bytes = (uint32_t)KS * (a.a_bytes + a.b_bytes);
+    a.stage_tx = (uint32_t)(kCtas * KS) *
                  ((w4 ? a.a_bytes / 2 : a.a_bytes) + (x4 ? a.b_bytes / 2 : a.b_bytes));
     a.slot_tx = (uint32_t)(a_rows + a.cap) * 16u;
     a.raw_b = a.cap > 128 ? 4096u : 2048u;
@@ -678,10 +669,10 @@ moe_status launch_expert_mx(const uint8_t *xq, const uint8_t *xs, int32_t x_fmt,
     CUtensorMap mw0, mw1, mw0s, mw1s, mx, mxs;
     const int64_t wrows = (int64_t)a.E * a.N;
     const int64_t Kp = mx_padded(K), sp = mx_scale_bytes(K);
-    const int w_k = GATE_UP ? 1 : a.ks;  // gate and up tiles alternate: one K block a load
+    const int w_k = GATE_UP ? 1 : KS;  // gate and up tiles alternate: one K block a load
     if (!make_mx_map(&mw0, w0, wrows, Kp, w4, a.ft, w_k) ||
         !make_byte_map(&mw0s, w0s, wrows, sp, a.ft) ||
-        !make_mx_map(&mx, xq, a.rows, Kp, x4, b_rows, a.ks) ||
+        !make_mx_map(&mx, xq, a.rows, Kp, x4, b_rows, KS) ||
         !make_byte_map(&mxs, xs, a.rows, sp, a.cap))
         return MOE_ERR_CUDA;
     mw1 = mw0;
@@ -689,7 +680,7 @@ moe_status launch_expert_mx(const uint8_t *xq, const uint8_t *xs, int32_t x_fmt,
     if (GATE_UP && (!make_mx_map(&mw1, w1, wrows, Kp, w4, a.ft, w_k) ||
                     !make_byte_map(&mw1s, w1s, wrows, sp, a.ft)))
         return MOE_ERR_CUDA;
-    if (cudaFuncSetAttribute(expert_mx_kernel<GATE_UP, PAIR>,
+    if (cudaFuncSetAttribute(expert_mx_kernel<GATE_UP, PAIR, KS>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
         cudaSuccess) {
         cudaGetLastError();
@@ -708,7 +699,7 @@ moe_status launch_expert_mx(const uint8_t *xq, const uint8_t *xs, int32_t x_fmt,
         attr[1].val.clusterDim.z = 1;
         cfg.numAttrs = 2;
     }
-    if (cudaLaunchKernelEx(&cfg, expert_mx_kernel<GATE_UP, PAIR>, mw0, mw1, mw0s, mw1s, mx, mxs,
+    if (cudaLaunchKernelEx(&cfg, expert_mx_kernel<GATE_UP, PAIR, KS>, mw0, mw1, mw0s, mw1s, mx, mxs,
                            a) != cudaSuccess) {
         cudaGetLastError();
         return MOE_ERR_CUDA;
@@ -728,15 +719,16 @@ moe_status run_expert_mx(const uint8_t *xq, const uint8_t *xs, int32_t x_fmt, co
     if (share <= 32) {
         // four times the average: few experts need a second part, which reads the weights again
         a.cap = share <= 4 ? 16 : share <= 8 ? 32 : share <= 16 ? 64 : 128;
-        a.ks = a.cap <= 64 ? 2 : 1;
         a.slots = 4;
-        return launch_expert_mx<GATE_UP, false>(xq, xs, x_fmt, w0, w0s, w1, w1s, w_fmt, K, a,
-                                                stream);
+        if (a.cap <= 64)
+            return launch_expert_mx<GATE_UP, false, 2>(xq, xs, x_fmt, w0, w0s, w1, w1s, w_fmt, K, a,
+                                                       stream);
+        return launch_expert_mx<GATE_UP, false, 1>(xq, xs, x_fmt, w0, w0s, w1, w1s, w_fmt, K, a,
+                                                   stream);
     }
     a.cap = share <= 64 ? 128 : 224;
-    a.ks = 1;
     a.slots = 3;
-    return launch_expert_mx<GATE_UP, true>(xq, xs, x_fmt, w0, w0s, w1, w1s, w_fmt, K, a, stream);
+    return launch_expert_mx<GATE_UP, true, 1>(xq, xs, x_fmt, w0, w0s, w1, w1s, w_fmt, K, a, stream);
 }
 
 moe_status check_ffn_mx(const void *x, const void *xs, int32_t x_fmt, int32_t w_fmt,

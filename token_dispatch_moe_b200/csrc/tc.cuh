@@ -227,30 +227,31 @@ __device__ __forceinline__ uint32_t mx_idesc_at(uint32_t idesc, uint32_t n, uint
     return idesc | ((n >> 3) << 17) | (k << 29) | (k << 4);
 }
 
-__device__ __forceinline__ void umma_mx(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
+// Descriptors as words: the low one holds the start address, the high one (hi) is constant.
+// PAIR: 256 rows of A over the CTA pair, B split between the CTAs by rows, and in each CTA's
+// TMEM the scales of its own 128 rows of A and of all N rows of B.
+template <bool PAIR>
+__device__ __forceinline__ void umma_mx(uint32_t tmem_d, uint32_t a_lo, uint32_t b_lo, uint32_t hi,
                                         uint32_t idesc, uint32_t sfa, uint32_t sfb,
                                         uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X"
-        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(tmem_d),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-        : "memory");
-}
-
-// ... of a CTA pair: 256 rows of A, B split between the CTAs by rows, and in each CTA's TMEM
-// the scales of its own 128 rows of A and of all N rows of B.
-__device__ __forceinline__ void umma_mx_pair(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
-                                             uint32_t idesc, uint32_t sfa, uint32_t sfb,
-                                             uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X"
-        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(tmem_d),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-        : "memory");
+    if (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+            "setp.ne.b32 p, %7, 0;\n\t"
+            "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X"
+            " [%0], da, db, %4, [%5], [%6], p;\n\t}" ::"r"(tmem_d),
+            "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+            "setp.ne.b32 p, %7, 0;\n\t"
+            "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X"
+            " [%0], da, db, %4, [%5], [%6], p;\n\t}" ::"r"(tmem_d),
+            "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
 }
 
 // Descriptor of 512 bytes of scales (32 rows of 16 bytes, laid end to end): no
@@ -263,16 +264,22 @@ __device__ __forceinline__ uint64_t scales_desc(uint32_t saddr) {
     d |= (uint64_t)1 << 46;
     return d;
 }
-// ... to four TMEM columns, repeated in the four lane quarters.
-__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t desc) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
-                 : "memory");
-}
-
-// ... in both CTAs of a pair, each from its own shared memory at this offset.
-__device__ __forceinline__ void tmem_cp_scales_pair(uint32_t taddr, uint64_t desc) {
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
-                 : "memory");
+// ... to four TMEM columns, repeated in the four lane quarters (PAIR: in both CTAs, each from
+// its own shared memory at this offset).
+template <bool PAIR>
+__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint32_t lo, uint32_t hi) {
+    if (PAIR)
+        asm volatile(
+            "{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\t"
+            "tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], d;\n\t}" ::"r"(taddr),
+            "r"(lo), "r"(hi)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\t"
+            "tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], d;\n\t}" ::"r"(taddr),
+            "r"(lo), "r"(hi)
+            : "memory");
 }
 
 // Arrival on an mbarrier of either CTA of the pair (bar: shared::cluster address).
