@@ -141,7 +141,9 @@ def _stream(stream):
     A torch stream of another device than the current one is refused: the
     library launches on the current device, with its kernels reading the
     tensors' addresses there."""
-    s = torch.cuda.current_stream() if stream is None else stream
+    if stream is None:  # the raw handle, without building a torch.cuda.Stream (3 us of a small call)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    s = stream
     if hasattr(s, "device") and s.device.index != torch.cuda.current_device():
         raise ValueError(f"stream is on {s.device}, the current device is "
                          f"cuda:{torch.cuda.current_device()}")
@@ -450,18 +452,27 @@ def moe_mx_row_bytes(K: int, format: int) -> tuple[int, int]:
     return row.value, scale.value
 
 
+_mx_bytes: dict = {}  # (K, format) -> bytes of a row's elements and scales
+
+
 def _need_mx(mx, name, ndim=2):
     """Checks MX rows' tensors; the leading sizes are returned."""
     q, scales, K, fmt = mx
-    _need(q, torch.uint8, name, ndim)
-    _need(scales, torch.uint8, f"{name} scales", ndim)
-    if K < 8 or K % 8 or fmt not in (MOE_MX_E4M3, MOE_MX_E2M1):
-        raise ValueError(f"{name}: K must be a multiple of 8 and the format E4M3 or E2M1")
-    padded = (K + 127) // 128 * 128
-    if q.shape[-1] != (padded if fmt == MOE_MX_E4M3 else padded // 2) or \
-            scales.shape[-1] != (padded // 32 + 15) // 16 * 16 or q.shape[:-1] != scales.shape[:-1]:
+    if q.dtype is not torch.uint8 or scales.dtype is not torch.uint8:
+        raise TypeError(f"{name} must be {torch.uint8}, got {q.dtype} and {scales.dtype}")
+    dev = torch.cuda.current_device() if q.is_cuda and scales.is_cuda else -1
+    if dev < 0 or q.get_device() != dev or scales.get_device() != dev or \
+            not q.is_contiguous() or not scales.is_contiguous():
+        _need(q, torch.uint8, name)
+        _need(scales, torch.uint8, f"{name} scales")
+    sizes = _mx_bytes.get((K, fmt))
+    if sizes is None:
+        sizes = _mx_bytes[(K, fmt)] = moe_mx_row_bytes(K, fmt)
+    qs, ss = q.shape, scales.shape
+    lead = qs[:-1]
+    if len(qs) != ndim or qs[-1] != sizes[0] or ss[-1] != sizes[1] or ss[:-1] != lead:
         raise ValueError(f"{name}: shape mismatch")
-    return q.shape[:-1]
+    return lead
 
 
 def moe_mx_quantize(x, out: MxRows, stream=None):

@@ -21,6 +21,7 @@
 //   warp 3     turns raw scale rows [row][16 bytes] into the tiles that TMEM
 //              wants (32 x 16 bytes, four rows' words side by side)
 //   warp 1     scale tiles to TMEM (tcgen05.cp) and four MMAs for every 128 K values
+//   warp 12    walks the tiles and hands them to the other roles through a ring
 //   warps 4-11 epilogue: TMEM -> shared memory, transposed to token-major; each
 //              thread then takes 8 features of a token: bias, activation, MX
 //              block (four lanes) or bf16, and one vector store
@@ -38,11 +39,13 @@
 namespace moe {
 namespace {
 
-constexpr int kXThreads = 384;
+constexpr int kXThreads = 416;
 constexpr int kXBK = 128;           // K values of a stage
 constexpr int kXSuper = 4;          // stages that one load of scales covers
 constexpr int kXMaxE = 4096;
+constexpr int kXMaxSmem = 227 * 1024;  // of a CTA on sm_100
 constexpr int kXMaxStages = 12;
+constexpr int kXBars = 512;  // bytes of barriers, the TMEM address and the tile ring
 constexpr int kXEpiThreads = 256;
 constexpr int kXChunk = 32;         // token columns the epilogue turns at a time,
 constexpr int kXChunkHalf = 16;     // half of them by each of a quarter's two warps
@@ -70,7 +73,7 @@ struct MxFfnArgs {
     int cap;                 // most tokens of a tile; also the columns of an accumulator
     int num_kb, stages, slots, tmem_cols, act, h_fmt;
     uint32_t a_bytes, b_bytes;     // a K block's weight and token tile in shared memory
-    uint32_t stage_bytes;          // KS of both
+    uint32_t stage_bytes;          // both
     uint32_t stage_tx, slot_tx;    // bytes their barriers count: 4-bit values packed
     uint32_t raw_b, tiled_b, slot_bytes, idesc;
     uint32_t sf, stg, bars, tables;  // offsets in shared memory (the stages come first)
@@ -186,6 +189,40 @@ struct Walk {
     }
 };
 
+// Tiles come from the walking warp in a ring of kXTiles; a role takes the next one as its own
+// copy and frees the place.  n = 0: no more tiles.
+constexpr int kXTiles = 4;
+struct TileRing {
+    const int4 *slots;
+    uint32_t there, taken;  // barriers of place 0
+    int32_t *status;
+    int at = 0;
+    uint32_t pass = 0;
+
+    __device__ __forceinline__ bool wait() {
+        return mbar_wait(there + 8u * (uint32_t)at, pass, status);
+    }
+    __device__ __forceinline__ Tile read() const {
+        const int4 v = slots[at];
+        return Tile{v.x, v.y, v.z, v.w};
+    }
+    __device__ __forceinline__ void free() {  // by every thread that counts as a reader
+        mbar_arrive(taken + 8u * (uint32_t)at);
+    }
+    __device__ __forceinline__ void next() {
+        at = (at + 1) & (kXTiles - 1);
+        if (at == 0) pass ^= 1u;
+    }
+    // For a role of one thread.
+    __device__ __forceinline__ bool take(Tile &w) {
+        if (!wait()) return false;
+        w = read();
+        free();
+        next();
+        return true;
+    }
+};
+
 // A K block's tile of an operand's rows.
 template <bool PAIR>
 __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap *map, uint32_t bar,
@@ -222,7 +259,7 @@ struct Ring {
     }
 };
 
-template <bool GATE_UP, bool PAIR, int KS>
+template <bool GATE_UP, bool PAIR>
 __global__ void __launch_bounds__(kXThreads, 1)
     expert_mx_kernel(const __grid_constant__ CUtensorMap map_w0,
                      const __grid_constant__ CUtensorMap map_w1,
@@ -248,7 +285,11 @@ __global__ void __launch_bounds__(kXThreads, 1)
     auto tfull_bar = [&](int b) { return bar0 + 8u * (2 * S + 3 * R + b); };
     auto tempty_bar = [&](int b) { return bar0 + 8u * (2 * S + 3 * R + 2 + b); };  // the leader's
     const uint32_t drain_bar = bar0 + 8u * (2 * S + 3 * R + 4);
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + a.bars + 8u * (2 * S + 3 * R + 5));
+    const uint32_t there_bar = bar0 + 8u * (2 * S + 3 * R + 5);  // [kXTiles]
+    const uint32_t taken_bar = there_bar + 8u * kXTiles;         // [kXTiles]
+    uint32_t *tmem_slot =
+        reinterpret_cast<uint32_t *>(gbase + a.bars + 8u * (2 * S + 3 * R + 5 + 2 * kXTiles));
+    int4 *tile_slots = reinterpret_cast<int4 *>(gbase + a.bars + kXBars - 16 * kXTiles);
     int32_t *off = reinterpret_cast<int32_t *>(gbase + a.tables);
     int32_t *parts = off + a.E + 1;
 
@@ -268,6 +309,12 @@ __global__ void __launch_bounds__(kXThreads, 1)
             mbar_init(tempty_bar(b), 8 * kCtas);  // each CTA's epilogue warps
         }
         mbar_init(drain_bar, 1);
+        for (int i = 0; i < kXTiles; ++i) {
+            mbar_init(there_bar + 8u * i, 1);
+            // readers: the two loading threads, the turning warp, the epilogue's eight warps,
+            // and the thread that issues the products
+            mbar_init(taken_bar + 8u * i, rank == 0 ? 12 : 11);
+        }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 2) {
@@ -320,42 +367,34 @@ __global__ void __launch_bounds__(kXThreads, 1)
     if (any_bad && threadIdx.x == 0 && blockIdx.x == 0) report(a.status, MOE_ERR_DEVICE_INDEX);
     volatile int *abort_v = &abort_s;
     griddep_launch_dependents();
+    TileRing tiles{tile_slots, there_bar, taken_bar, a.status};
 
     // The producers and the MMA issuer are one thread each, and their loops are unrolled over
     // the K blocks that a load of scales covers: what bounds them is the length of the chain
     // of instructions between two issues.
     if (warp == 0) {
         if (elect_one()) {
-            Walk walk(a, off, parts, kCtas, rank);
             Tile w;
             Ring st;
             uint32_t filled = 0;
             bool ok = true;
             const uint32_t lead_full = PAIR ? cluster_map(full_bar(0), 0) : full_bar(0);
             const uint32_t up = (uint32_t)a.ft * 128u;
-            for (; ok && !*abort_v && walk.tile(w); walk.next()) {
+            while (ok && !*abort_v) {
+                ok = tiles.take(w);
+                if (!ok || w.n == 0) break;
                 const int wrow = w.e * a.N + w.f0;
                 // a pair's tokens in multiples of 16: each CTA holds one half's rows
                 const int xrow = w.row0 + (PAIR ? rank * (((w.n + 15) & ~15) >> 1) : 0);
-                for (int kb = 0; kb < a.num_kb; kb += KS) {
+                for (int kb = 0; kb < a.num_kb; ++kb) {
                     ok = mbar_wait(empty_bar(st.at), st.pass ^ 1u, a.status);
                     if (!ok) break;
-                    uint32_t dst = base + (uint32_t)st.at * a.stage_bytes;
+                    const uint32_t dst = base + (uint32_t)st.at * a.stage_bytes;
                     const uint32_t bar = lead_full + 8u * (uint32_t)st.at;
                     if (rank == 0) mbar_arrive_expect_tx(full_bar(st.at), a.stage_tx);
-                    // K blocks behind the last are filled with zeros (and not multiplied)
-                    if (GATE_UP) {
-#pragma unroll
-                        for (int i = 0; i < KS; ++i) {
-                            load_tile<PAIR>(dst, &map_w0, bar, wrow, kb + i);
-                            load_tile<PAIR>(dst + up, &map_w1, bar, wrow, kb + i);
-                            dst += a.a_bytes;
-                        }
-                    } else {
-                        load_tile<PAIR>(dst, &map_w0, bar, wrow, kb);
-                        dst += (uint32_t)KS * a.a_bytes;
-                    }
-                    load_tile<PAIR>(dst, &map_x, bar, xrow, kb);
+                    load_tile<PAIR>(dst, &map_w0, bar, wrow, kb);
+                    if (GATE_UP) load_tile<PAIR>(dst + up, &map_w1, bar, wrow, kb);
+                    load_tile<PAIR>(dst + a.a_bytes, &map_x, bar, xrow, kb);
                     st.next(S);
                     ++filled;
                 }
@@ -370,7 +409,6 @@ __global__ void __launch_bounds__(kXThreads, 1)
         }
     } else if (warp == 1) {
         if (rank == 0 && elect_one()) {
-            Walk walk(a, off, parts, kCtas, rank);
             Tile w;
             Ring st, sf, acc;
             bool ok = true;
@@ -378,11 +416,13 @@ __global__ void __launch_bounds__(kXThreads, 1)
             // descriptors: only the start address, in the low word, differs
             const uint64_t d0 = sw128_desc(base), s0 = scales_desc(base + a.sf + 2048u + a.raw_b);
             const uint32_t d_hi = (uint32_t)(d0 >> 32), s_hi = (uint32_t)(s0 >> 32);
-            const uint32_t a16 = a.a_bytes >> 4, b16 = a.b_bytes >> 4;
+            const uint32_t a16 = a.a_bytes >> 4;
             const uint32_t stage16 = a.stage_bytes >> 4, slot16 = a.slot_bytes >> 4;
             const uint32_t tiled16 = a.tiled_b >> 4;
             uint32_t d_lo = (uint32_t)d0, s_lo = (uint32_t)s0;  // of the ring places in use
-            for (; ok && !*abort_v && walk.tile(w); walk.next()) {
+            while (ok && !*abort_v) {
+                ok = tiles.take(w);
+                if (!ok || w.n == 0) break;
                 const uint32_t n = PAIR ? (uint32_t)(w.n + 15) & ~15u : (uint32_t)(w.n + 7) & ~7u;
                 uint32_t idesc[4];
 #pragma unroll
@@ -393,41 +433,41 @@ __global__ void __launch_bounds__(kXThreads, 1)
                 tc_fence_after();
                 const uint32_t d = tmem_base + (uint32_t)(acc.at * a.cap);
                 uint32_t more = 0;
-                for (int left = a.num_kb; left > 0; left -= kXSuper) {
-                    ok = mbar_wait(ready_bar(sf.at), sf.pass, a.status);
-                    if (!ok) break;
+                // The four K blocks of a load of scales (fewer behind K's end); false if a wait
+                // gave up.
+                auto super = [&](int blocks) -> bool {
+                    if (!mbar_wait(ready_bar(sf.at), sf.pass, a.status)) return false;
+                    tc_fence_after();
 #pragma unroll
                     for (int q = 0; q < kXSuper; ++q) {
-                        if (q >= left) break;
-                        if (q % KS == 0) {
-                            ok = mbar_wait(full_bar(st.at), st.pass, a.status);
-                            if (!ok) break;
-                            tc_fence_after();
-                        }
+                        if (q >= blocks) break;
+                        if (!mbar_wait(full_bar(st.at), st.pass, a.status)) return false;
+                        tc_fence_after();
+                        // scales' columns begin at multiples of four
                         const uint32_t sfa = sf_col + 16u * (q & 1), sfb = sfa + 4u;
                         const uint32_t sb = s_lo + 128u + (uint32_t)q * tiled16;
                         tmem_cp_scales<PAIR>(sfa, s_lo + 32u * q, s_hi);
                         tmem_cp_scales<PAIR>(sfb, sb, s_hi);
                         if (wide) tmem_cp_scales<PAIR>(sfb + 4u, sb + 32u, s_hi);
-                        const uint32_t a_lo = d_lo + (uint32_t)(q % KS) * a16;
-                        const uint32_t b_lo = d_lo + (uint32_t)KS * a16 + (uint32_t)(q % KS) * b16;
+                        const uint32_t b_lo = d_lo + a16;
 #pragma unroll
                         for (uint32_t k = 0; k < 4; ++k) {
-                            umma_mx<PAIR>(d, a_lo + 2u * k, b_lo + 2u * k, d_hi, idesc[k], sfa, sfb,
+                            umma_mx<PAIR>(d, d_lo + 2u * k, b_lo + 2u * k, d_hi, idesc[k], sfa, sfb,
                                           more);
                             more = 1u;
                         }
-                        if (q % KS == KS - 1 || q + 1 == left) {
-                            commit<PAIR>(empty_bar(st.at));
-                            st.next(S);
-                            d_lo = st.at == 0 ? (uint32_t)d0 : d_lo + stage16;
-                        }
+                        commit<PAIR>(empty_bar(st.at));
+                        st.next(S);
+                        d_lo = st.at == 0 ? (uint32_t)d0 : d_lo + stage16;
                     }
-                    if (!ok) break;
                     commit<PAIR>(free_bar(sf.at));
                     sf.next(R);
                     s_lo = sf.at == 0 ? (uint32_t)s0 : s_lo + slot16;
-                }
+                    return true;
+                };
+                int left = a.num_kb;
+                for (; ok && left >= kXSuper; left -= kXSuper) ok = super(kXSuper);
+                if (ok && left > 0) ok = super(left);
                 if (!ok) break;
                 commit<PAIR>(tfull_bar(acc.at));
                 acc.next(2);
@@ -439,12 +479,13 @@ __global__ void __launch_bounds__(kXThreads, 1)
         }
     } else if (warp == 2) {
         if (elect_one()) {
-            Walk walk(a, off, parts, kCtas, rank);
             Tile w;
             Ring sf;
             uint32_t filled = 0;
             bool ok = true;
-            for (; ok && !*abort_v && walk.tile(w); walk.next()) {
+            while (ok && !*abort_v) {
+                ok = tiles.take(w);
+                if (!ok || w.n == 0) break;
                 const int wrow = w.e * a.N + w.f0;
                 for (int c = 0; c < a.num_kb; c += kXSuper) {
                     ok = mbar_wait(free_bar(sf.at), sf.pass ^ 1u, a.status);
@@ -466,21 +507,26 @@ __global__ void __launch_bounds__(kXThreads, 1)
             }
         }
     } else if (warp == 3) {
-        Walk walk(a, off, parts, kCtas, rank);
-        Tile w;
         Ring sf;
         const int supers = (a.num_kb + kXSuper - 1) / kXSuper;
         bool ok = true;
         const uint32_t lead_ready = PAIR ? cluster_map(ready_bar(0), 0) : ready_bar(0);
-        for (; ok && !*abort_v && walk.tile(w); walk.next()) {
+        while (ok && !*abort_v) {
+            ok = __all_sync(MOE_FULL_MASK, tiles.wait());
+            if (!ok) break;
+            const Tile w = tiles.read();
+            __syncwarp();
+            if (lane == 0) tiles.free();
+            tiles.next();
+            if (w.n == 0) break;
             for (int c = 0; c < supers; ++c) {
                 ok = __all_sync(MOE_FULL_MASK, mbar_wait(raw_bar(sf.at), sf.pass, a.status));
                 if (!ok) break;
                 uint8_t *sl = gbase + a.sf + (size_t)sf.at * a.slot_bytes;
-                uint8_t *tiles = sl + 2048 + a.raw_b;
-                turn_scales(sl, tiles, 512u, lane);
-                turn_scales(sl + 2048, tiles + 2048, a.tiled_b, lane);
-                if (w.n > 128) turn_scales(sl + 4096, tiles + 2560, a.tiled_b, lane);
+                uint8_t *turned = sl + 2048 + a.raw_b;
+                turn_scales(sl, turned, 512u, lane);
+                turn_scales(sl + 2048, turned + 2048, a.tiled_b, lane);
+                if (w.n > 128) turn_scales(sl + 4096, turned + 2560, a.tiled_b, lane);
                 fence_async_shared();
                 __syncwarp();
                 if (lane == 0) {
@@ -493,6 +539,21 @@ __global__ void __launch_bounds__(kXThreads, 1)
             }
         }
         if (!ok) *abort_v = 1;
+    } else if (warp == 12) {
+        if (lane == 0) {
+            Walk walk(a, off, parts, kCtas, rank);
+            Tile w;
+            Ring to;
+            for (bool any = true; any && !*abort_v; walk.next(), to.next(kXTiles)) {
+                any = walk.tile(w);
+                if (!mbar_wait(taken_bar + 8u * (uint32_t)to.at, to.pass ^ 1u, a.status)) {
+                    *abort_v = 1;
+                    break;
+                }
+                tile_slots[to.at] = make_int4(w.e, w.row0, any ? w.n : 0, w.f0);
+                mbar_arrive(there_bar + 8u * (uint32_t)to.at);
+            }
+        }
     } else {
         // Two warps share a quarter of the TMEM lanes, half of a chunk's token columns each.
         // gate_up: the 32 gate features of quarter q and the same up features, ft / 32 quarters
@@ -507,17 +568,16 @@ __global__ void __launch_bounds__(kXThreads, 1)
         constexpr int kPitch = kXPitch[GATE_UP], kBuffer = kXBuffer[GATE_UP];
         float *stg = reinterpret_cast<float *>(gbase + a.stg) +
                      (2 * duo + half) * ((GATE_UP ? 2 : 1) * kBuffer);
-        Walk walk(a, off, parts, kCtas, rank);
-        Tile w;
         Ring acc;
         const int grp = lane & 3;  // 8 of the block's features
         const int cover = a.f_tiles * kCtas * a.ft;  // features of all tiles, N or a little more
         const uint32_t lead_tempty = PAIR ? cluster_map(tempty_bar(0), 0) : tempty_bar(0);
         int buf = 0;
-        for (; walk.tile(w); walk.next()) {
+        for (;;) {
             // One thread polls; the others wait at the barrier that carries its answer.
-            int ok = threadIdx.x != 128 ||
-                     (!*abort_v && mbar_wait(tfull_bar(acc.at), acc.pass, a.status));
+            int ok = threadIdx.x != 128 || (!*abort_v && tiles.wait() &&
+                                            (tiles.read().n == 0 ||
+                                             mbar_wait(tfull_bar(acc.at), acc.pass, a.status)));
             asm volatile(
                 "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %0, 0;\n\t"
                 "barrier.red.and.pred q, 1, %1, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
@@ -528,6 +588,11 @@ __global__ void __launch_bounds__(kXThreads, 1)
                 *abort_v = 1;
                 break;
             }
+            const Tile w = tiles.read();
+            __syncwarp();
+            if (lane == 0) tiles.free();
+            tiles.next();
+            if (w.n == 0) break;
             tc_fence_after();
             const uint32_t trow = tmem_base + (uint32_t)(acc.at * a.cap) +
                                   ((uint32_t)(q * 32) << 16) + (uint32_t)(kXChunkHalf * half);
@@ -622,7 +687,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
     }
 }
 
-template <bool GATE_UP, bool PAIR, int KS>
+template <bool GATE_UP, bool PAIR>
 moe_status launch_expert_mx(const uint8_t *xq, const uint8_t *xs, int32_t x_fmt, const uint8_t *w0,
                             const uint8_t *w0s, const uint8_t *w1, const uint8_t *w1s,
                             int32_t w_fmt, int32_t K, MxFfnArgs a, moe_stream_t stream) {
@@ -633,8 +698,8 @@ moe_status launch_expert_mx(const uint8_t *xq, const uint8_t *xs, int32_t x_fmt,
     const int a_rows = (GATE_UP ? 2 : 1) * a.ft, b_rows = a.cap / kCtas;
     a.a_bytes = (uint32_t)a_rows * 128u;
     a.b_bytes = (uint32_t)b_rows * 128u;
-    a.stage_bytes = (uint32_t)KS * (a.a_bytes + a.b_bytes);
-    a.stage_tx = (uint32_t)(kCtas * KS) *
+    a.stage_bytes = a.a_bytes + a.b_bytes;
+    a.stage_tx = (uint32_t)kCtas *
                  ((w4 ? a.a_bytes / 2 : a.a_bytes) + (x4 ? a.b_bytes / 2 : a.b_bytes));
     a.slot_tx = (uint32_t)(a_rows + a.cap) * 16u;
     a.raw_b = a.cap > 128 ? 4096u : 2048u;
@@ -644,18 +709,11 @@ moe_status launch_expert_mx(const uint8_t *xq, const uint8_t *xs, int32_t x_fmt,
     int cols = 32;
     while (cols < 2 * a.cap + 32) cols *= 2;
     a.tmem_cols = cols;
-    int dev = 0, max_smem = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&max_smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) !=
-            cudaSuccess) {
-        cudaGetLastError();
-        return MOE_ERR_CUDA;
-    }
-    const uint32_t stg = kXStageBytes[GATE_UP], bars = 512;
+    const uint32_t stg = kXStageBytes[GATE_UP], bars = kXBars;
     const uint32_t tables = ((uint32_t)(2 * (a.E + 1)) * 4u + 15u) / 16u * 16u;
     // alignment slack, static shared memory; MMAs read 128 weight rows where a tile has fewer:
     // what lies behind the stages is large enough for that
-    const int64_t rest = (int64_t)max_smem - 1024 - 64 - stg - bars - tables -
+    const int64_t rest = (int64_t)kXMaxSmem - 1024 - 64 - stg - bars - tables -
                          (int64_t)a.slots * a.slot_bytes;
     int64_t stages = rest / a.stage_bytes;
     if (stages > kXMaxStages) stages = kXMaxStages;
@@ -669,18 +727,17 @@ moe_status launch_expert_mx(const uint8_t *xq, const uint8_t *xs, int32_t x_fmt,
     CUtensorMap mw0, mw1, mw0s, mw1s, mx, mxs;
     const int64_t wrows = (int64_t)a.E * a.N;
     const int64_t Kp = mx_padded(K), sp = mx_scale_bytes(K);
-    const int w_k = GATE_UP ? 1 : KS;  // gate and up tiles alternate: one K block a load
-    if (!make_mx_map(&mw0, w0, wrows, Kp, w4, a.ft, w_k) ||
+    if (!make_mx_map(&mw0, w0, wrows, Kp, w4, a.ft) ||
         !make_byte_map(&mw0s, w0s, wrows, sp, a.ft) ||
-        !make_mx_map(&mx, xq, a.rows, Kp, x4, b_rows, KS) ||
+        !make_mx_map(&mx, xq, a.rows, Kp, x4, b_rows) ||
         !make_byte_map(&mxs, xs, a.rows, sp, a.cap))
         return MOE_ERR_CUDA;
     mw1 = mw0;
     mw1s = mw0s;
-    if (GATE_UP && (!make_mx_map(&mw1, w1, wrows, Kp, w4, a.ft, w_k) ||
+    if (GATE_UP && (!make_mx_map(&mw1, w1, wrows, Kp, w4, a.ft) ||
                     !make_byte_map(&mw1s, w1s, wrows, sp, a.ft)))
         return MOE_ERR_CUDA;
-    if (cudaFuncSetAttribute(expert_mx_kernel<GATE_UP, PAIR, KS>,
+    if (cudaFuncSetAttribute(expert_mx_kernel<GATE_UP, PAIR>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
         cudaSuccess) {
         cudaGetLastError();
@@ -699,7 +756,7 @@ moe_status launch_expert_mx(const uint8_t *xq, const uint8_t *xs, int32_t x_fmt,
         attr[1].val.clusterDim.z = 1;
         cfg.numAttrs = 2;
     }
-    if (cudaLaunchKernelEx(&cfg, expert_mx_kernel<GATE_UP, PAIR, KS>, mw0, mw1, mw0s, mw1s, mx, mxs,
+    if (cudaLaunchKernelEx(&cfg, expert_mx_kernel<GATE_UP, PAIR>, mw0, mw1, mw0s, mw1s, mx, mxs,
                            a) != cudaSuccess) {
         cudaGetLastError();
         return MOE_ERR_CUDA;
@@ -707,9 +764,14 @@ moe_status launch_expert_mx(const uint8_t *xq, const uint8_t *xs, int32_t x_fmt,
     return launch_status();
 }
 
-// Tile shape by the rows an expert has on average.  With few, the weights' bytes are the time:
-// narrow token tiles leave shared memory to weight stages of two K blocks.  With many, the
-// products are: pairs of CTAs, each holding half of the tokens.
+// Tile shape by the rows an expert has on average.  A wider token tile takes shared memory from
+// the weights in flight; a narrower one cuts more blocks into parts, each of which reads the
+// weights again.  About twice the average is best; pairs of CTAs (half of the tokens' bytes per
+// CTA) from where products count.  Measured with 128 experts of 2880 x 2880, e2m1 weights,
+// gate_up in us, by rows an expert (cap 16, 32, 64; pairs with 64, 128, 224):
+//     8:  189  197  217 |  226  268  301        64:  770  433  320 |  334  269  306
+//    16:  238  201  218 |  230  264  316       128: 1390  748  500 |  491  383  365
+//    32:  389  274  230 |  236  271  312
 template <bool GATE_UP>
 moe_status run_expert_mx(const uint8_t *xq, const uint8_t *xs, int32_t x_fmt, const uint8_t *w0,
                          const uint8_t *w0s, const uint8_t *w1, const uint8_t *w1s, int32_t w_fmt,
@@ -717,18 +779,14 @@ moe_status run_expert_mx(const uint8_t *xq, const uint8_t *xs, int32_t x_fmt, co
     const int64_t share = (a.rows + a.E - 1) / a.E;
     a.ft = GATE_UP ? 64 : 128;
     if (share <= 32) {
-        // four times the average: few experts need a second part, which reads the weights again
-        a.cap = share <= 4 ? 16 : share <= 8 ? 32 : share <= 16 ? 64 : 128;
+        a.cap = share <= 8 ? 16 : share <= 16 ? 32 : 64;
         a.slots = 4;
-        if (a.cap <= 64)
-            return launch_expert_mx<GATE_UP, false, 2>(xq, xs, x_fmt, w0, w0s, w1, w1s, w_fmt, K, a,
-                                                       stream);
-        return launch_expert_mx<GATE_UP, false, 1>(xq, xs, x_fmt, w0, w0s, w1, w1s, w_fmt, K, a,
-                                                   stream);
+        return launch_expert_mx<GATE_UP, false>(xq, xs, x_fmt, w0, w0s, w1, w1s, w_fmt, K, a,
+                                                stream);
     }
-    a.cap = share <= 64 ? 128 : 224;
+    a.cap = share <= 96 ? 128 : 224;
     a.slots = 3;
-    return launch_expert_mx<GATE_UP, true, 1>(xq, xs, x_fmt, w0, w0s, w1, w1s, w_fmt, K, a, stream);
+    return launch_expert_mx<GATE_UP, true>(xq, xs, x_fmt, w0, w0s, w1, w1s, w_fmt, K, a, stream);
 }
 
 moe_status check_ffn_mx(const void *x, const void *xs, int32_t x_fmt, int32_t w_fmt,

@@ -370,17 +370,17 @@ inline bool make_byte_map(CUtensorMap *m, const void *ptr, int64_t rows, int64_t
 }
 
 // Element rows [rows][cols] of an MX operand (cols a multiple of 128) as a 3-D tensor
-// [cols / 128][rows][128], box = box_k x box_rows x 128, 128-byte swizzle: box_k tiles of
-// box_rows rows in one load.  e4m3: bytes.  e2m1: packed in memory (32-byte aligned), widened
-// to 8-bit containers in shared memory (16 values: 8 packed bytes and 8 unused).
+// [cols / 128][rows][128], box = 1 x box_rows x 128, 128-byte swizzle.  e4m3: bytes.  e2m1:
+// packed in memory (32-byte aligned), widened to 8-bit containers in shared memory (16 values:
+// 8 packed bytes and 8 unused); a barrier counts the packed bytes.
 inline bool make_mx_map(CUtensorMap *m, const void *ptr, int64_t rows, int64_t cols, bool packed,
-                        int box_rows, int box_k) {
+                        int box_rows) {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return false;
     const cuuint64_t pitch = (cuuint64_t)(packed ? cols / 2 : cols);
     cuuint64_t dims[3] = {128u, (cuuint64_t)rows, (cuuint64_t)cols / 128};
     cuuint64_t strides[2] = {pitch, packed ? 64u : 128u};
-    cuuint32_t box[3] = {128u, (cuuint32_t)box_rows, (cuuint32_t)box_k};
+    cuuint32_t box[3] = {128u, (cuuint32_t)box_rows, 1u};
     cuuint32_t estr[3] = {1, 1, 1};
     return enc(m, packed ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
                const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
