@@ -101,13 +101,11 @@ __global__ void __launch_bounds__(256) add_rmsnorm_kernel(const NormArgs a) {
         }
         if (FMT >= 0) {
             constexpr int F = FMT < 0 ? 0 : FMT;
-            unpack_bf16x8(y, f);
             uint32_t byte;
-            const uint2 e = mx_quarter<F>(f, byte);
+            const uint2 e = mx_quarter_bf16<F>(y, byte);
             uint8_t *srow = a.scales + row * a.scale_bytes;
             if (v < a.padded) mx_store<F>(a.q + row * a.row_bytes, srow, v, e, byte);
-            if (v + 1 == a.padded)
-                for (int64_t b = a.padded / 4; b < a.scale_bytes; ++b) srow[b] = 0;
+            if (v + 1 == a.padded) mx_clear_scales(srow, a.padded / 4, a.scale_bytes);
         }
     }
 }

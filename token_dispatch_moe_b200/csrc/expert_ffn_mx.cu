@@ -662,7 +662,8 @@ __global__ void __launch_bounds__(kXThreads, 1)
                     uint8_t *qrow = a.hq + row * a.h_row, *srow = a.hs + row * a.h_scale;
                     for (int64_t k = a.h_fmt == MOE_MX_E4M3 ? cover : cover / 2; k < a.h_row; k += 16)
                         *reinterpret_cast<uint4 *>(qrow + k) = make_uint4(0u, 0u, 0u, 0u);
-                    for (int64_t k = cover / kMxBlock; k < a.h_scale; ++k) srow[k] = 0;
+                    for (int64_t k = cover / kMxBlock; k < a.h_scale; k += 2)
+                        *reinterpret_cast<uint16_t *>(srow + k) = 0;
                 }
             }
             acc.next(2);

@@ -103,16 +103,52 @@ __device__ __forceinline__ uint2 mx_quarter(const float (&v)[8], uint32_t &byte)
     return byte == 255u ? make_uint2(0u, 0u) : q;
 }
 
-// The lane's elements at vector `vec` (8 values) of a row, and by the first
-// lane of each four the block's scale.
+// The same of 8 bf16 values.  Magnitudes are compared as 16-bit integers, two at a time, and
+// the power of two is multiplied in bf16, which is exact down to products so small that
+// they round to zero elements anyhow.
 template <int FMT>
-__device__ __forceinline__ void mx_store(uint8_t *row, uint8_t *scales, int vec, uint2 q,
-                                         uint32_t byte) {
+__device__ __forceinline__ uint2 mx_quarter_bf16(const uint4 &in, uint32_t &byte) {
+    const uint32_t u[4] = {in.x, in.y, in.z, in.w};
+    uint32_t m2 = u[0] & 0x7fff7fffu;
+#pragma unroll
+    for (int i = 1; i < 4; ++i)
+        asm("max.u16x2 %0, %0, %1;" : "+r"(m2) : "r"(u[i] & 0x7fff7fffu));
+    asm("max.u16x2 %0, %0, %1;" : "+r"(m2) : "r"(__shfl_xor_sync(MOE_FULL_MASK, m2, 1)));
+    asm("max.u16x2 %0, %0, %1;" : "+r"(m2) : "r"(__shfl_xor_sync(MOE_FULL_MASK, m2, 2)));
+    byte = mx_scale_byte<FMT>(max(m2 << 16, m2 & 0xffff0000u));
+    const uint32_t inv = ((254u - byte) & 0xffu) * 0x00800080u;
+    float s[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t p;
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(p) : "r"(u[i]), "r"(inv));
+        s[2 * i] = __uint_as_float(p << 16);
+        s[2 * i + 1] = __uint_as_float(p & 0xffff0000u);
+    }
+    const uint2 q = mx_pack8<FMT>(s);
+    return byte == 255u ? make_uint2(0u, 0u) : q;
+}
+
+// The lane's elements at vector `vec` (8 values) of a row.
+template <int FMT>
+__device__ __forceinline__ void mx_store_elements(uint8_t *row, int vec, uint2 q) {
     if (FMT == MOE_MX_E4M3)
         *reinterpret_cast<uint2 *>(row + 8 * (int64_t)vec) = q;
     else
         *reinterpret_cast<uint32_t *>(row + 4 * (int64_t)vec) = q.x;
+}
+
+// ... and by the first lane of each four the block's scale.
+template <int FMT>
+__device__ __forceinline__ void mx_store(uint8_t *row, uint8_t *scales, int vec, uint2 q,
+                                         uint32_t byte) {
+    mx_store_elements<FMT>(row, vec, q);
     if ((vec & 3) == 0) scales[vec >> 2] = (uint8_t)byte;
+}
+
+// Zeros behind the scales of a row's blocks (both counts are multiples of four).
+__device__ __forceinline__ void mx_clear_scales(uint8_t *scales, int64_t blocks, int64_t bytes) {
+    for (int64_t b = blocks; b < bytes; b += 4) *reinterpret_cast<uint32_t *>(scales + b) = 0u;
 }
 
 __device__ __forceinline__ void unpack_bf16x8(const uint4 &v, float (&f)[8]) {

@@ -3,9 +3,11 @@
 // Both are one pass over the data, bound by memory: a value costs 2 bytes on
 // the bf16 side and 1 + 1/32 (e4m3) or 1/2 + 1/32 (e2m1) on the other.  A
 // lane takes 8 values (16 bytes of bf16); four lanes hold a block and find its
-// largest magnitude with two shuffles.  A block of threads takes a run of
-// kRowVecs vectors of the rows laid end to end (padding included), kRowUnroll
-// of them a thread, all loads issued before the first use.
+// largest magnitude with two shuffles.  A warp takes kRowUnroll * 32
+// consecutive vectors of the rows laid end to end (quantize: padding
+// included), all its loads issued before the first use, so its scales are 32
+// consecutive bytes: they go out in one store (one byte store a vector
+// row of a warp held quantize at 5.0 TB/s).
 #include <cuda_fp16.h>
 
 #include "mx.cuh"
@@ -15,95 +17,110 @@ namespace moe {
 namespace {
 
 constexpr int kRowThreads = 256;
-constexpr int kRowUnroll = 4;
+constexpr int kRowUnroll = 4;  // 32 blocks a warp: one lane for each scale
 constexpr int kRowVecs = kRowThreads * kRowUnroll;
 
 struct MxRowsArgs {
     int64_t vecs;      // rows * vpr
-    uint32_t vpr;      // 8-value vectors of a padded row
-    uint32_t magic;    // floor(2^32 / vpr) + 1: x / vpr = umulhi(x, magic) while x * vpr < 2^32,
-                       // and x < vpr + kRowVecs with vpr <= 2^15; not used with vpr 1
+    uint32_t vpr;      // 8-value vectors of a row: with its padding (quantize) or without
+    uint32_t magic;    // floor(2^32 / vpr) + 1: v / vpr = umulhi(v, magic) for v * vpr < 2^32, so
+                       // for v < vpr + kRowVecs (vpr <= 2^15); not used with vpr 1
     uint32_t data;     // vectors of a row that hold data
     int64_t row_bytes, scale_bytes;
 };
 
-// Row and vector of element `off` of the run that starts at (row0, vec0).
-__device__ __forceinline__ int64_t place(const MxRowsArgs &a, int64_t row0, uint32_t vec0,
-                                         uint32_t off, uint32_t &vec) {
-    const uint32_t x = vec0 + off;
-    const uint32_t r = a.vpr == 1 ? x : __umulhi(x, a.magic);
-    vec = x - r * a.vpr;
-    return row0 + r;
-}
+// Row and vector of the warp's vector `off` places on from its first.
+struct Place {
+    int64_t row;
+    uint32_t vec;
+    __device__ __forceinline__ Place(const MxRowsArgs &a, uint32_t off) {
+        const int64_t i = (int64_t)blockIdx.x * kRowVecs;
+        row = i / a.vpr;  // the same for the block
+        vec = (uint32_t)(i - row * a.vpr) + (threadIdx.x >> 5) * (32 * kRowUnroll) + off;
+        const uint32_t r = rows_on(a, vec);
+        row += r;
+        vec -= r * a.vpr;
+    }
+    static __device__ __forceinline__ uint32_t rows_on(const MxRowsArgs &a, uint32_t v) {
+        return a.vpr == 1 ? v : __umulhi(v, a.magic);
+    }
+};
 
 template <int FMT>
 __global__ void __launch_bounds__(kRowThreads)
     mx_quantize_kernel(const moe_bf16_t *__restrict__ x, uint8_t *__restrict__ q,
                        uint8_t *__restrict__ scales, const MxRowsArgs a) {
     griddep_wait();
-    const int64_t base = (int64_t)blockIdx.x * kRowVecs;
-    const int64_t row0 = base / a.vpr;
-    const uint32_t vec0 = (uint32_t)(base - row0 * a.vpr);
+    const uint32_t lane = threadIdx.x & 31;
+    const int64_t base =
+        (int64_t)blockIdx.x * kRowVecs + (threadIdx.x >> 5) * (32 * kRowUnroll) + lane;
+    const int left = (int)min(a.vecs - base, (int64_t)kRowVecs);  // this lane's u runs while 32 u < left
     uint4 in[kRowUnroll];
-    int64_t row[kRowUnroll];
-    uint32_t vec[kRowUnroll];
+    if (a.data == a.vpr) {  // no padding: x is as flat as the elements
+        const uint4 *src = reinterpret_cast<const uint4 *>(x) + base;
 #pragma unroll
-    for (int u = 0; u < kRowUnroll; ++u) {
-        const uint32_t off = u * kRowThreads + threadIdx.x;
-        row[u] = place(a, row0, vec0, off, vec[u]);
-        in[u] = make_uint4(0u, 0u, 0u, 0u);
-        if (base + off < a.vecs && vec[u] < a.data)
-            in[u] = ld_stream(reinterpret_cast<const uint4 *>(x) + row[u] * a.data + vec[u]);
+        for (int u = 0; u < kRowUnroll; ++u)
+            in[u] = 32 * u < left ? ld_stream(src + 32 * u) : make_uint4(0u, 0u, 0u, 0u);
+    } else {
+        const Place at(a, lane);
+        const int gap = (int)(a.vpr - a.data);
+        const uint4 *src = reinterpret_cast<const uint4 *>(x) + base - at.row * gap;
+#pragma unroll
+        for (int u = 0; u < kRowUnroll; ++u) {
+            const uint32_t v = at.vec + 32 * u, r = Place::rows_on(a, v);
+            in[u] = make_uint4(0u, 0u, 0u, 0u);
+            if (32 * u < left && v - r * a.vpr < a.data) in[u] = ld_stream(src + (32 * u - (int)r * gap));
+        }
     }
     griddep_launch_dependents();
+    uint32_t mine = 0;  // scale of the warp's block number `lane`
+    uint8_t *dst = q + base * (FMT == MOE_MX_E4M3 ? 8 : 4);  // element rows follow without gaps
 #pragma unroll
     for (int u = 0; u < kRowUnroll; ++u) {
-        const uint32_t off = u * kRowThreads + threadIdx.x;
-        float f[8];
-        unpack_bf16x8(in[u], f);
         uint32_t byte;
-        const uint2 e = mx_quarter<FMT>(f, byte);  // four lanes of a block share its fate
-        if (base + off >= a.vecs) continue;
-        uint8_t *srow = scales + row[u] * a.scale_bytes;
-        mx_store<FMT>(q + row[u] * a.row_bytes, srow, (int)vec[u], e, byte);
-        // the bytes behind the last block's scale
-        if (vec[u] + 1 == a.vpr)
-            for (int64_t b = a.vpr / 4; b < a.scale_bytes; ++b) srow[b] = 0;
+        const uint2 e = mx_quarter_bf16<FMT>(in[u], byte);
+        const uint32_t from = __shfl_sync(MOE_FULL_MASK, byte, 4 * (lane & 7));
+        if ((lane >> 3) == u) mine = from;
+        if (32 * u < left) mx_store_elements<FMT>(dst, 32 * u, e);
     }
+    if (3 * (int)lane >= left) return;  // vector 4 * lane of the warp lies behind the last
+    const Place block(a, 4 * lane);
+    uint8_t *srow = scales + block.row * a.scale_bytes;
+    srow[block.vec >> 2] = (uint8_t)mine;
+    if (block.vec + 4 == a.vpr) mx_clear_scales(srow, a.vpr / 4, a.scale_bytes);
 }
 
 template <int FMT>
 __global__ void __launch_bounds__(kRowThreads)
     mx_dequantize_kernel(const uint8_t *__restrict__ q, const uint8_t *__restrict__ scales,
                          moe_bf16_t *__restrict__ out, const MxRowsArgs a) {
-    // Here vpr counts the vectors that hold data: padding is not read.
     griddep_wait();
-    const int64_t base = (int64_t)blockIdx.x * kRowVecs;
-    const int64_t row0 = base / a.vpr;
-    const uint32_t vec0 = (uint32_t)(base - row0 * a.vpr);
+    const uint32_t lane = threadIdx.x & 31;
+    const int64_t base =
+        (int64_t)blockIdx.x * kRowVecs + (threadIdx.x >> 5) * (32 * kRowUnroll) + lane;
+    const int left = (int)min(a.vecs - base, (int64_t)kRowVecs);  // this lane's u runs while 32 u < left
+    const Place at(a, lane);
+    const uint8_t *qrow = q + at.row * a.row_bytes, *srow = scales + at.row * a.scale_bytes;
     uint2 in[kRowUnroll];
     uint32_t byte[kRowUnroll];
 #pragma unroll
     for (int u = 0; u < kRowUnroll; ++u) {
-        const uint32_t off = u * kRowThreads + threadIdx.x;
-        uint32_t vec;
-        const int64_t row = place(a, row0, vec0, off, vec);
+        const uint32_t x = at.vec + 32 * u, r = Place::rows_on(a, x), vec = x - r * a.vpr;
         in[u] = make_uint2(0u, 0u);
         byte[u] = 0;
-        if (base + off < a.vecs) {
-            const uint8_t *src = q + row * a.row_bytes;
+        if (32 * u < left) {
+            const uint8_t *src = qrow + r * a.row_bytes;
             if (FMT == MOE_MX_E4M3)
                 in[u] = __ldcs(reinterpret_cast<const uint2 *>(src) + vec);
             else
                 in[u].x = __ldcs(reinterpret_cast<const uint32_t *>(src) + vec);
-            byte[u] = __ldg(scales + row * a.scale_bytes + (vec >> 2));
+            byte[u] = __ldg(srow + r * a.scale_bytes + (vec >> 2));
         }
     }
     griddep_launch_dependents();
 #pragma unroll
     for (int u = 0; u < kRowUnroll; ++u) {
-        const int64_t i = base + u * kRowThreads + threadIdx.x;
-        if (i >= a.vecs) continue;
+        if (32 * u >= left) continue;
         const float s = mx_scale(byte[u]);
         float f[8];
 #pragma unroll
@@ -123,7 +140,7 @@ __global__ void __launch_bounds__(kRowThreads)
             f[2 * p] = v.x * s;
             f[2 * p + 1] = v.y * s;
         }
-        reinterpret_cast<uint4 *>(out)[i] = pack_bf16x8(f);  // rows of out have no padding
+        reinterpret_cast<uint4 *>(out)[base + 32 * u] = pack_bf16x8(f);  // rows of out have no padding
     }
 }
 
