@@ -9,10 +9,11 @@ from __future__ import annotations
 
 import torch
 
-from . import (MOE_ACT_SWIGLU, MOE_ACT_SWIGLU_OAI, RouteParams, moe_combine, moe_dispatch,
-               moe_dispatch_limited, moe_dispatch_limited_rows, moe_dispatch_workspace_size,
-               moe_expert_down, moe_expert_gate_up, moe_gate_gemm, moe_gate_route,
-               moe_hash_route, moe_permute, moe_route)
+from . import (MOE_ACT_SWIGLU, MOE_ACT_SWIGLU_OAI, MxRows, RouteParams, moe_add_rmsnorm,
+               moe_combine, moe_dispatch, moe_dispatch_limited, moe_dispatch_limited_rows,
+               moe_dispatch_workspace_size, moe_expert_down, moe_expert_down_mx,
+               moe_expert_gate_up, moe_expert_gate_up_mx, moe_gate_gemm, moe_gate_route,
+               moe_hash_route, moe_mx_quantize, moe_permute, moe_route)
 from .workloads import Workload
 
 
@@ -20,7 +21,7 @@ class RouterDispatch:
     """Preallocated buffers for T tokens of one layer configuration."""
 
     def __init__(self, wl: Workload, device="cuda", n_rows: int | None = None,
-                 fused: bool | None = None, keep_logits: bool = False):
+                 fused: bool | None = None, keep_logits: bool = False, mx: int | None = None):
         """fused: gate workloads route inside the gate GEMM (moe_gate_route)
         when the configuration allows it (k_max <= 16); None picks it where it
         measured faster: a gate workload with neither a group limit nor a
@@ -29,7 +30,10 @@ class RouterDispatch:
         k_max = 16 when most tokens take 4 or 8, cost more there than the
         separate route kernel spread over the whole GPU.)
         keep_logits: also write the logits (parity checks need them; the fused
-        path skips them otherwise)."""
+        path skips them otherwise).
+        mx: microscaled format (MOE_MX_E4M3, MOE_MX_E2M1) of the activations; the
+        experts' FFN then takes MX operands (weights as make_mx_expert_weights
+        lays them out), over the dispatch's blocks as they are."""
         self.wl = wl
         if fused is None:
             fused = wl.n_groups == 1 and wl.k_choices is None
@@ -56,7 +60,8 @@ class RouterDispatch:
         ws = moe_dispatch_workspace_size(T, k, E)
         self.workspace = torch.empty((max(ws, 256),), dtype=torch.uint8, device=device)
         rows = self.expert_rows if n_rows is None else n_rows
-        self.xs = torch.empty((max(rows, 1), wl.d), dtype=torch.bfloat16, device=device)
+        self.xs = (torch.empty((max(rows, 1), wl.d), dtype=torch.bfloat16, device=device)
+                   if mx is None else None)
         self.out = (torch.empty((T, wl.d), dtype=torch.bfloat16, device=device)
                     if wl.combine else None)
         self.status = torch.zeros((1,), **i32)
@@ -66,6 +71,15 @@ class RouterDispatch:
                                  device=device)
             self.y = torch.empty((max(self.expert_rows, 1), wl.d), dtype=torch.bfloat16,
                                  device=device)
+        self.mx = mx
+        if mx is not None:
+            if not wl.ffn_dim:
+                raise ValueError(f"{wl.name} has no expert FFN shape")
+            self.xn = torch.empty((T, wl.d), dtype=torch.bfloat16, device=device)
+            self.x_mx = MxRows.empty((T,), wl.d, mx, device)
+            self.xs_mx = MxRows.empty((max(rows, 1),), wl.d, mx, device)
+            self.h_mx = MxRows.empty((max(rows, 1),), wl.ffn_dim, mx, device)
+            self.y = torch.empty((max(rows, 1), wl.d), dtype=torch.bfloat16, device=device)
         if wl.hash_vocab:
             self.hash_ids = torch.empty((T, k), **i32)
             self.hash_w = torch.empty((T, k), dtype=torch.float32, device=device)
@@ -112,28 +126,63 @@ class RouterDispatch:
         moe_expert_down(self.h, self.offsets, weights["w2"], self.y, weights["b2"], self.status,
                         stream)
 
+    def norm(self, x, residual, gain, eps=1e-5, residual_out=None, stream=None):
+        """The norm in front of the gate: self.xn, its MX rows self.x_mx, and the
+        residual stream x + residual to residual_out."""
+        moe_add_rmsnorm(x, residual, gain, eps, residual_out, self.xn, self.x_mx, stream)
+        return self.xn
+
+    def permute_mx(self, stream=None):
+        """x_mx into expert order: elements and scales are byte rows to moe_permute."""
+        for src, dst in zip(self.x_mx.as_bf16_rows(), self.xs_mx.as_bf16_rows()):
+            moe_permute(src, self.dest_pos, dst, stream)
+
+    def expert_gate_up_mx(self, weights: dict, stream=None):
+        act = MOE_ACT_SWIGLU_OAI if self.wl.ffn_act == "swiglu_oai" else MOE_ACT_SWIGLU
+        moe_expert_gate_up_mx(self.xs_mx, self.offsets, weights["w1"], weights["w3"], self.h_mx,
+                              weights["b1"], weights["b3"], act, self.status, stream)
+
+    def expert_down_mx(self, weights: dict, stream=None):
+        moe_expert_down_mx(self.h_mx, self.offsets, weights["w2"], self.y, weights["b2"],
+                           self.status, stream)
+
     # The whole chain -----------------------------------------------------------
     def run(self, inputs: dict, stream=None, experts: dict | None = None):
-        """gate (if the workload has one) -> route -> dispatch -> permute ->
-        [experts' FFN, when ``experts`` holds their weights] -> combine (if the
-        workload ends there).  ``inputs`` as made by :func:`workloads.make_inputs`;
-        without experts the combine reads the synthetic ``inputs["y"]``."""
+        """[norm, with ``inputs["gain"]``] -> gate (if the workload has one) -> route ->
+        dispatch -> permute -> [experts' FFN, when ``experts`` holds their weights] ->
+        combine (if the workload ends there).  ``inputs`` as made by
+        :func:`workloads.make_inputs`; without experts the combine reads the synthetic
+        ``inputs["y"]``.  With MX activations, ``inputs["gain"]`` (and ``"residual"``,
+        ``"residual_out"``, ``"eps"``) put the norm in front; without it x is quantised as
+        it is."""
+        x = inputs["x"]
+        if self.mx is not None:
+            if inputs.get("gain") is not None:
+                x = self.norm(x, inputs.get("residual"), inputs["gain"], inputs.get("eps", 1e-5),
+                              inputs.get("residual_out"), stream)
+            else:
+                moe_mx_quantize(x, self.x_mx, stream)
         if self.fused:
-            self.gate_route(inputs["x"], inputs["w"], inputs["bias"], inputs["k_per_token"], stream)
+            self.gate_route(x, inputs["w"], inputs["bias"], inputs["k_per_token"], stream)
         else:
-            logits = (self.gate(inputs["x"], inputs["w"], stream) if self.wl.gate
-                      else inputs["logits"])
+            logits = self.gate(x, inputs["w"], stream) if self.wl.gate else inputs["logits"]
             self.route(logits, inputs["bias"], inputs["k_per_token"], stream)
         self.dispatch(stream=stream)
-        self.permute(inputs["x"], stream)
         y = inputs["y"]
-        if experts is not None:
+        if self.mx is None:
+            self.permute(x, stream)
+        else:
+            self.permute_mx(stream)
+            self.expert_gate_up_mx(experts, stream)
+            self.expert_down_mx(experts, stream)
+            y = self.y
+        if experts is not None and self.mx is None:
             self.expert_gate_up(experts, stream)
             self.expert_down(experts, stream)
             y = self.y
         if self.wl.combine:
             self.combine(y, inputs["shared"], stream)
-        return self.out if self.wl.combine else self.xs
+        return self.out if self.wl.combine else (self.xs if self.mx is None else self.y)
 
     def run_hash_layer(self, inputs: dict, logits=None, stream=None):
         """hash_route -> dispatch -> permute (the hash-routed layer's chain)."""

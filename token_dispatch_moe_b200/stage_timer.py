@@ -16,7 +16,10 @@ package's own.  route_grouped runs moe_route_grouped on the route's logits,
 with the workload's groups (8 where it has none) and --kpg candidates a group.
 expert_gate_up and expert_down run the experts' FFN GEMMs (workloads with an
 FFN shape; expert blocks padded to 128 rows, synthetic weights) on the
-permuted rows, and print TFLOP/s beside the bytes.
+permuted rows, and print TFLOP/s beside the bytes.  norm is moe_add_rmsnorm on
+the workload's rows (with a residual, bf16 and MX outputs), mx_quantize
+moe_mx_quantize on them; expert_gate_up_mx and expert_down_mx the experts' FFN on
+MX operands over unpadded blocks.  --mx and --mx-weights: the formats (e4m3, e2m1).
 """
 from __future__ import annotations
 
@@ -27,7 +30,9 @@ import statistics
 import torch
 
 STAGES = ("gate_gemm", "gate_route", "route", "route_grouped", "hash_route", "dispatch", "permute",
-          "combine", "expert_gate_up", "expert_down")
+          "combine", "expert_gate_up", "expert_down", "norm", "mx_quantize", "expert_gate_up_mx",
+          "expert_down_mx")
+MX_STAGES = STAGES[-4:]
 
 
 def main(argv=None):
@@ -40,6 +45,8 @@ def main(argv=None):
     ap.add_argument("--lib", default=None)
     ap.add_argument("--kpg", type=int, default=2,
                     help="route_grouped: candidates a group (groups: the workload's, else 8)")
+    ap.add_argument("--mx", default="e4m3", choices=("e4m3", "e2m1"))
+    ap.add_argument("--mx-weights", default="e2m1", choices=("e4m3", "e2m1"))
     args = ap.parse_args(argv)
 
     import token_dispatch_moe_b200 as moe
@@ -56,14 +63,20 @@ def main(argv=None):
         wl = wl.scaled(args.tokens)
     st = args.stage
     experts = None
-    if st.startswith("expert_"):
+    mx_format = {"e4m3": moe.MOE_MX_E4M3, "e2m1": moe.MOE_MX_E2M1}
+    mx = mx_format[args.mx] if st in MX_STAGES else None
+    if mx is not None and st.startswith("expert_"):
+        from token_dispatch_moe_b200.workloads import make_mx_expert_weights
+        experts = make_mx_expert_weights(wl, mx_format[args.mx_weights], device)
+    elif st.startswith("expert_"):
         from token_dispatch_moe_b200.workloads import make_expert_weights
         wl = wl.with_ffn()
         experts = make_expert_weights(wl, device)
-    need_x = wl.gate or st in ("permute", "expert_gate_up", "expert_down")
+    need_x = wl.gate or mx is not None or st in ("permute", "expert_gate_up", "expert_down")
     inp = make_inputs(wl, device, with_y=(st == "combine"), with_x=need_x)
     fused = st == "gate_route"
-    path = RouterDispatch(wl, device, fused=fused, keep_logits=not fused)
+    path = RouterDispatch(wl, device, fused=fused, keep_logits=not fused,
+                          mx=mx if experts is not None else None)
     n_assign = num_assignments(wl, inp["k_per_token"])
 
     logits = inp["logits"]
@@ -72,10 +85,19 @@ def main(argv=None):
     if st in ("dispatch", "permute", "combine") or experts is not None:
         path.route(logits, inp["bias"], inp["k_per_token"])
         path.dispatch()
-    if experts is not None:
+    if experts is not None and mx is not None:
+        moe.moe_mx_quantize(inp["x"], path.x_mx)
+        path.permute_mx()
+        path.expert_gate_up_mx(experts)
+    elif experts is not None:
         path.permute(inp["x"])
         path.expert_gate_up(experts)
-    if st != "permute" and not wl.gate:
+    if mx is not None and experts is None:
+        rows = moe.MxRows.empty((wl.T,), wl.d, mx, device)
+        residual, h, y = (torch.empty_like(inp["x"]) for _ in range(3))
+        residual.normal_()
+        gain = torch.ones((wl.d,), dtype=torch.bfloat16, device=device)
+    if st != "permute" and not wl.gate and mx is None:
         inp["x"] = None
     torch.cuda.synchronize()
 
@@ -89,6 +111,10 @@ def main(argv=None):
         "combine": lambda: path.combine(inp["y"], inp["shared"]),
         "expert_gate_up": lambda: path.expert_gate_up(experts),
         "expert_down": lambda: path.expert_down(experts),
+        "norm": lambda: moe.moe_add_rmsnorm(inp["x"], residual, gain, 1e-5, h, y, rows),
+        "mx_quantize": lambda: moe.moe_mx_quantize(inp["x"], rows),
+        "expert_gate_up_mx": lambda: path.expert_gate_up_mx(experts),
+        "expert_down_mx": lambda: path.expert_down_mx(experts),
     }
     if st == "route_grouped":
         G = wl.n_groups if wl.n_groups > 1 else 8
@@ -119,9 +145,17 @@ def main(argv=None):
             times.append(e0.elapsed_time(e1) * 1e3)
     model = hash_stage_bytes(wl) if st == "hash_route" else stage_bytes(wl, n_assign, fused)
     model["route_grouped"] = wl.T * (4 * wl.E + 8 * wl.k_max)  # logits in, ids and weights out
+    flops = dict(stage_flops(wl, n_assign))
+    if mx is not None:
+        a, w = ({"e4m3": 1, "e2m1": 0.5}[f] + 1 / 32 for f in (args.mx, args.mx_weights))
+        T, d, E, F, n = wl.T, wl.d, wl.E, wl.ffn_dim, n_assign
+        model.update(norm=T * d * (8 + a), mx_quantize=T * d * (2 + a),
+                     expert_gate_up_mx=n * d * a + 2 * E * F * d * w + n * F * a,
+                     expert_down_mx=n * F * a + E * d * F * w + 2 * n * d)
+        flops.update(expert_gate_up_mx=4.0 * n * d * F, expert_down_mx=2.0 * n * d * F)
     us = statistics.fmean(times)
     nbytes = model.get(st)
-    flops = stage_flops(wl, n_assign).get(st)
+    flops = flops.get(st)
     print(json.dumps({
         "workload": wl.name, "tokens": wl.T, "stage": st, "lib": args.lib or "package",
         "us": round(us, 2), "us_min": round(min(times), 2), "iters": args.iters,

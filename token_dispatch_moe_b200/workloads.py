@@ -139,6 +139,18 @@ def make_expert_weights(wl: Workload, device="cuda", seed_offset: int = 0) -> di
     return out
 
 
+def make_mx_expert_weights(wl: Workload, format: int, device="cuda", seed_offset: int = 0) -> dict:
+    """make_expert_weights with the three matrices as MX rows of the given format (quantised
+    on the GPU); the biases as they are."""
+    from . import MxRows, moe_mx_quantize
+    out = make_expert_weights(wl, device, seed_offset)
+    for name in ("w1", "w3", "w2"):
+        w = out[name]
+        out[name] = MxRows.empty(w.shape[:-1], w.shape[-1], format, device)
+        moe_mx_quantize(w, out[name])
+    return out
+
+
 def k_per_token(wl: Workload, device, seed=None):
     """k_t for every token: one draw from wl.k_choices per request segment."""
     if wl.k_choices is None:
