@@ -126,7 +126,7 @@ def test_quantize_past_32_bits():
 
 
 NORM_CASES = [(1, 8), (1, 2880), (3, 40), (17, 128), (5, 2048), (9, 2056), (2, 7168), (4, 4104),
-              (2, 16384), (300, 264)]
+              (2, 16384), (300, 264), (33, 16), (19, 256), (21, 512), (9, 1024), (5, 1032)]
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
@@ -176,6 +176,7 @@ def test_norm_rows_of_zeros_and_nan():
     y = y.cpu()
     assert torch.isfinite(y[:2]).all() and not y[1].any()
     assert torch.isnan(y[2]).all() and torch.isnan(y[3, 70])
+    assert not y[3, :70].any() and y[3, 71] == 0
     assert_bits(mx, y)
 
 

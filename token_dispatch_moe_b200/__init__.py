@@ -142,7 +142,7 @@ def _stream(stream):
     library launches on the current device, with its kernels reading the
     tensors' addresses there."""
     if stream is None:  # the raw handle, without building a torch.cuda.Stream (3 us of a small call)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(_current_device())
     s = stream
     if hasattr(s, "device") and s.device.index != torch.cuda.current_device():
         raise ValueError(f"stream is on {s.device}, the current device is "
@@ -155,8 +155,13 @@ def _check(status: int, where: str):
         raise MoeError(status, where)
 
 
+# The current device without the Python layers around it (a call here checks up to ten tensors).
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _need(t, dtype, name, ndim=None):
-    if t is None:
+    if t is None or (t.dtype is dtype and t.is_cuda and t.get_device() == _current_device() and
+                     t.is_contiguous() and (ndim is None or t.dim() == ndim)):
         return
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -460,7 +465,7 @@ def _need_mx(mx, name, ndim=2):
     q, scales, K, fmt = mx
     if q.dtype is not torch.uint8 or scales.dtype is not torch.uint8:
         raise TypeError(f"{name} must be {torch.uint8}, got {q.dtype} and {scales.dtype}")
-    dev = torch.cuda.current_device() if q.is_cuda and scales.is_cuda else -1
+    dev = _current_device() if q.is_cuda and scales.is_cuda else -1
     if dev < 0 or q.get_device() != dev or scales.get_device() != dev or \
             not q.is_contiguous() or not scales.is_contiguous():
         _need(q, torch.uint8, name)

@@ -79,19 +79,32 @@ struct MxFfnArgs {
     uint32_t sf, stg, bars, tables;  // offsets in shared memory (the stages come first)
 };
 
-// As in the bf16 kernel's epilogue: fast exponential and quotient, about 1e-6
-// relative, far below the rounding to 8 bits.
+// e^-x to a few units of fp32: 2^t with t = -x log2(e) rounded, times what the rounding of t
+// and of log2(e) lost (to first order).  Without that factor the error grows with |x|, to
+// 1e-6 at |x| = 10: no matter to the value of h, but ten times as many of its roundings (and
+// of its blocks' powers of two) would fall on the other side than the exact sum's.
+__device__ __forceinline__ float exp_neg(float x) {
+    constexpr float kL = 1.44269504f, kLLow = 1.92596299e-8f, kLn2 = 0.693147181f;
+    const float t = -x * kL;
+    const float lost = fmaf(-x, kLLow, fmaf(-x, kL, -t));
+    float p;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(t));
+    return p * fmaf(lost, kLn2, 1.0f);
+}
+
+// The quotient is the fast one (2 units of fp32); a denominator that overflows gives 0, the
+// limit for very negative gates.
 __device__ __forceinline__ void activate8(float (&g)[8], const float (&u)[8], int act) {
     if (act == MOE_ACT_SWIGLU_OAI) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             const float gc = fminf(g[k], kXOaiLimit);
             const float uc = fminf(fmaxf(u[k], -kXOaiLimit), kXOaiLimit);
-            g[k] = __fdividef(gc, 1.0f + __expf(-kXOaiAlpha * gc)) * (uc + 1.0f);
+            g[k] = __fdividef(gc, 1.0f + exp_neg(kXOaiAlpha * gc)) * (uc + 1.0f);
         }
     } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) g[k] = __fdividef(g[k], 1.0f + __expf(-g[k])) * u[k];
+        for (int k = 0; k < 8; ++k) g[k] = __fdividef(g[k], 1.0f + exp_neg(g[k])) * u[k];
     }
 }
 
