@@ -33,7 +33,6 @@
 // own 128 weight rows, half of the tokens' rows, and all of the tokens' scales.
 // Every wait is bounded, as in the bf16 kernels.
 #include "mx.cuh"
-#include "rows.cuh"
 #include "tc.cuh"
 
 namespace moe {
@@ -47,14 +46,13 @@ constexpr int kXMaxSmem = 227 * 1024;  // of a CTA on sm_100
 constexpr int kXMaxStages = 12;
 constexpr int kXBars = 512;  // bytes of barriers, the TMEM address and the tile ring
 constexpr int kXEpiThreads = 256;
-constexpr int kXChunk = 32;         // token columns the epilogue turns at a time,
-constexpr int kXChunkHalf = 16;     // half of them by each of a quarter's two warps
+constexpr int kXChunk = 64;         // token columns the epilogue turns at a time,
+constexpr int kXChunkHalf = 32;     // half of them by each of a quarter's two warps
 // Floats of a staged token: 16-byte aligned, the rows of eight reading lanes on different banks.
-// gate_up: 32 gate and 32 up values, two buffers of 16 tokens for each of the 4 pairs of warps;
-// down: 32 values, one buffer for each of the 8 warps.
+// gate_up: 32 gate and 32 up values, a buffer of 32 tokens for each of the 4 pairs of warps;
+// down: 32 values, a buffer for each of the 8 warps.
 constexpr int kXPitch[2] = {36, 68};
-constexpr int kXBuffer[2] = {16 * 36, 16 * 68};
-constexpr int kXStageBytes[2] = {8 * 16 * 36 * 4, 4 * 2 * 16 * 68 * 4};
+constexpr int kXStageBytes[2] = {8 * kXChunkHalf * 36 * 4, 4 * kXChunkHalf * 68 * 4};
 constexpr float kXOaiAlpha = 1.702f;
 constexpr float kXOaiLimit = 7.0f;
 
@@ -79,52 +77,70 @@ struct MxFfnArgs {
     uint32_t sf, stg, bars, tables;  // offsets in shared memory (the stages come first)
 };
 
-// e^-x to a few units of fp32: 2^t with t = -x log2(e) rounded, times what the rounding of t
-// and of log2(e) lost (to first order).  Without that factor the error grows with |x|, to
-// 1e-6 at |x| = 10: no matter to the value of h, but ten times as many of its roundings (and
-// of its blocks' powers of two) would fall on the other side than the exact sum's.
-__device__ __forceinline__ float exp_neg(float x) {
+// e^-x to a few units of fp32, two at a time: 2^t with t = -x log2(e) rounded, times what the
+// rounding of t and of log2(e) lost (to first order).  Without that factor the error grows with
+// |x|, to 1e-6 at |x| = 10: no matter to the value of h, but ten times as many of its roundings
+// (and of its blocks' powers of two) would fall on the other side than the exact sum's.  From
+// x = -200 down the result is infinite.
+__device__ __forceinline__ f32x2 exp_neg(f32x2 x) {
     constexpr float kL = 1.44269504f, kLLow = 1.92596299e-8f, kLn2 = 0.693147181f;
-    const float t = -x * kL;
-    const float lost = fmaf(-x, kLLow, fmaf(-x, kL, -t));
-    float p;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(t));
-    return p * fmaf(lost, kLn2, 1.0f);
+    const float2 v = halves(x);
+    const float a = fmaxf(v.x, -200.0f), b = fmaxf(v.y, -200.0f);
+    const float ta = -a * kL, tb = -b * kL;
+    const f32x2 lost = fma2(pair_of(a, b), pair_of(-kLLow, -kLLow),
+                            pair_of(fmaf(-a, kL, -ta), fmaf(-b, kL, -tb)));
+    float pa, pb;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(pa) : "f"(ta));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(pb) : "f"(tb));
+    return mul2(pair_of(pa, pb), fma2(lost, pair_of(kLn2, kLn2), pair_of(1.0f, 1.0f)));
 }
 
-// The quotient is the fast one (2 units of fp32); a denominator that overflows gives 0, the
-// limit for very negative gates.
-__device__ __forceinline__ void activate8(float (&g)[8], const float (&u)[8], int act) {
+// 1 / x by the hardware's estimate (one unit of fp32; 0 for an infinite x).
+__device__ __forceinline__ f32x2 reciprocal2(f32x2 x) {
+    float2 v = halves(x);
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(v.x));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(v.y));
+    return pair_of(v.x, v.y);
+}
+
+// g becomes act(g, u); a very negative gate gives 0, its limit.
+__device__ __forceinline__ void activate8(f32x2 (&g)[4], const f32x2 (&u)[4], int act) {
+    const f32x2 one = pair_of(1.0f, 1.0f);
     if (act == MOE_ACT_SWIGLU_OAI) {
+        const f32x2 alpha = pair_of(kXOaiAlpha, kXOaiAlpha);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float gc = fminf(g[k], kXOaiLimit);
-            const float uc = fminf(fmaxf(u[k], -kXOaiLimit), kXOaiLimit);
-            g[k] = __fdividef(gc, 1.0f + exp_neg(kXOaiAlpha * gc)) * (uc + 1.0f);
+        for (int k = 0; k < 4; ++k) {
+            const float2 a = halves(g[k]), b = halves(u[k]);
+            const f32x2 gc = pair_of(fminf(a.x, kXOaiLimit), fminf(a.y, kXOaiLimit));
+            const f32x2 uc = pair_of(fminf(fmaxf(b.x, -kXOaiLimit), kXOaiLimit),
+                                     fminf(fmaxf(b.y, -kXOaiLimit), kXOaiLimit));
+            const f32x2 rc = reciprocal2(add2(exp_neg(mul2(gc, alpha)), one));
+            g[k] = mul2(mul2(gc, rc), add2(uc, one));
         }
     } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) g[k] = __fdividef(g[k], 1.0f + exp_neg(g[k])) * u[k];
+        for (int k = 0; k < 4; ++k)
+            g[k] = mul2(mul2(g[k], reciprocal2(add2(exp_neg(g[k]), one))), u[k]);
     }
 }
 
-__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
-    const float4 x = *reinterpret_cast<const float4 *>(p);
-    const float4 y = *reinterpret_cast<const float4 *>(p + 4);
-    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-    v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+__device__ __forceinline__ void load8(const float *p, f32x2 (&v)[4]) {
+    const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(p);
+    const ulonglong2 y = *reinterpret_cast<const ulonglong2 *>(p + 4);
+    v[0] = x.x, v[1] = x.y;
+    v[2] = y.x, v[3] = y.y;
 }
 
 // 8 features of a row of h (four neighbouring lanes hold a block).
-__device__ __forceinline__ void store_h(const MxFfnArgs &a, int64_t row, int f, const float (&o)[8],
-                                        bool there) {
+__device__ __forceinline__ void store_h(const MxFfnArgs &a, int64_t row, int f, const f32x2 (&o)[4],
+                                        bool there, bool real) {
     uint8_t *qrow = a.hq + row * a.h_row, *srow = a.hs + row * a.h_scale;
     uint32_t byte;
     if (a.h_fmt == MOE_MX_E4M3) {
-        const uint2 e = mx_quarter<MOE_MX_E4M3>(o, byte);
+        const uint2 e = mx_quarter<MOE_MX_E4M3>(o, real, byte);
         if (there) mx_store<MOE_MX_E4M3>(qrow, srow, f >> 3, e, byte);
     } else {
-        const uint2 e = mx_quarter<MOE_MX_E2M1>(o, byte);
+        const uint2 e = mx_quarter<MOE_MX_E2M1>(o, real, byte);
         if (there) mx_store<MOE_MX_E2M1>(qrow, srow, f >> 3, e, byte);
     }
 }
@@ -578,14 +594,13 @@ __global__ void __launch_bounds__(kXThreads, 1)
         const int duo = GATE_UP ? q % up : q;  // block of 32 features
         const int member = GATE_UP && q >= up ? 1 : 0;
         const int bar_id = 2 + 2 * duo + half;
-        constexpr int kPitch = kXPitch[GATE_UP], kBuffer = kXBuffer[GATE_UP];
+        constexpr int kPitch = kXPitch[GATE_UP];
         float *stg = reinterpret_cast<float *>(gbase + a.stg) +
-                     (2 * duo + half) * ((GATE_UP ? 2 : 1) * kBuffer);
+                     (2 * duo + half) * (kXChunkHalf * kPitch);
         Ring acc;
         const int grp = lane & 3;  // 8 of the block's features
         const int cover = a.f_tiles * kCtas * a.ft;  // features of all tiles, N or a little more
         const uint32_t lead_tempty = PAIR ? cluster_map(tempty_bar(0), 0) : tempty_bar(0);
-        int buf = 0;
         for (;;) {
             // One thread polls; the others wait at the barrier that carries its answer.
             int ok = threadIdx.x != 128 || (!*abort_v && tiles.wait() &&
@@ -612,53 +627,71 @@ __global__ void __launch_bounds__(kXThreads, 1)
             const int f = w.f0 + 32 * duo + 8 * grp;
             const bool real_f = f < a.N;
             const int mine = w.n - kXChunkHalf * half;  // tokens from this half's first on
-            uint32_t v[kXChunkHalf];
-            if (works && mine > 0) tmem_ld16_nowait(trow, v);
-            float b0[8], b1[8];
+            // 32 columns as two loads, so that none reads behind the tile's
+            uint32_t v[2][16];
+            if (works && mine > 0) tmem_ld16_nowait(trow, v[0]);
+            if (works && mine > 16) tmem_ld16_nowait(trow + 16u, v[1]);
+            f32x2 b0[4], b1[4];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) b0[k] = b1[k] = 0.0f;
+            for (int k = 0; k < 4; ++k) b0[k] = b1[k] = 0ull;
             if (real_f && a.bias0) load8(a.bias0 + (int64_t)w.e * a.N + f, b0);
             if (GATE_UP && real_f && a.bias1) load8(a.bias1 + (int64_t)w.e * a.N + f, b1);
-            for (int c0 = 0; works && c0 < mine; c0 += kXChunk, buf ^= 1) {
-                // gate_up: two buffers and one meeting a chunk: whoever is past the meeting of
-                // the chunk before has read the chunk before that.
-                float *sb = stg + (GATE_UP ? buf * kBuffer : 0);
+            for (int c0 = 0; works && c0 < mine; c0 += kXChunk) {
+                auto meet = [&] {  // the warps that share the buffer
+                    if (GATE_UP)
+                        asm volatile("bar.sync %0, 64;" ::"r"(bar_id) : "memory");
+                    else
+                        __syncwarp();
+                };
                 tmem_wait_ld();
-                if (!GATE_UP) __syncwarp();
+                if (c0 > 0) meet();  // the last chunk has been read
 #pragma unroll
                 for (int i = 0; i < kXChunkHalf; ++i)
-                    sb[i * kPitch + 32 * member + lane] = __uint_as_float(v[i]);
-                if (c0 + kXChunk < mine) tmem_ld16_nowait(trow + (uint32_t)(c0 + kXChunk), v);
-                if (GATE_UP)
-                    asm volatile("bar.sync %0, 64;" ::"r"(bar_id) : "memory");
-                else
-                    __syncwarp();
-                // 16 tokens, four lanes each: 8 a warp (gate_up) or both eights (down)
+                    stg[i * kPitch + 32 * member + lane] = __uint_as_float(v[i >> 4][i & 15]);
+                if (c0 + kXChunk < mine) {
+                    tmem_ld16_nowait(trow + (uint32_t)(c0 + kXChunk), v[0]);
+                    if (c0 + kXChunk + 16 < mine)
+                        tmem_ld16_nowait(trow + (uint32_t)(c0 + kXChunk + 16), v[1]);
+                }
+                meet();
+                // 32 tokens, four lanes each: 16 a warp (gate_up) or all of them (down), two
+                // eights at a time
+                const int first = GATE_UP ? 16 * member : 0, tokens = GATE_UP ? 16 : 32;
+                for (int t0 = first; t0 < first + tokens && c0 + t0 < mine; t0 += 16) {
 #pragma unroll
-                for (int t8 = 0; t8 < (GATE_UP ? 1 : 2); ++t8) {
-                    const int tok = 8 * (GATE_UP ? member : t8) + (lane >> 2);
-                    const bool there = c0 + tok < mine;
-                    const int64_t row = (int64_t)w.row0 + kXChunkHalf * half + c0 + tok;
-                    const float *src = sb + tok * kPitch + 8 * grp;
-                    float o[8];
-                    load8(src, o);
+                    for (int t8 = 0; t8 < 16; t8 += 8) {
+                        const int tok = t0 + t8 + (lane >> 2);
+                        const bool there = c0 + tok < mine;
+                        const int64_t row = (int64_t)w.row0 + kXChunkHalf * half + c0 + tok;
+                        const float *src = stg + tok * kPitch + 8 * grp;
+                        f32x2 o[4];
+                        load8(src, o);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) o[k] += b0[k];
-                    if (GATE_UP) {
-                        float u[8];
-                        load8(src + 32, u);
+                        for (int k = 0; k < 4; ++k) o[k] = add2(o[k], b0[k]);
+                        if (GATE_UP) {
+                            f32x2 u[4];
+                            load8(src + 32, u);
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) u[k] += b1[k];
-                        activate8(o, u, a.act);
-                        // features behind N: zeros of the row's padding
+                            for (int k = 0; k < 4; ++k) u[k] = add2(u[k], b1[k]);
+                            activate8(o, u, a.act);
+                            // features behind N are zeros of the row's padding
+                            store_h(a, row, f, o, there, real_f && there);
+                        } else if (there && real_f) {
+                            uint32_t p[4];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) o[k] = real_f && there ? o[k] : 0.0f;
-                        store_h(a, row, f, o, there);
-                    } else if (there && real_f) {
-                        *reinterpret_cast<uint4 *>(a.y + row * a.N + f) = pack_bf16x8(o);
+                            for (int k = 0; k < 4; ++k) {
+                                const float2 v2 = halves(o[k]);
+                                const __nv_bfloat162 two = __floats2bfloat162_rn(v2.x, v2.y);
+                                p[k] = *reinterpret_cast<const uint32_t *>(&two);
+                            }
+                            *reinterpret_cast<uint4 *>(a.y + row * a.N + f) =
+                                make_uint4(p[0], p[1], p[2], p[3]);
+                        }
                     }
                 }
             }
+            // The buffer's last readers before the next tile's writers.
+            if (GATE_UP && works && mine > 0) asm volatile("bar.sync %0, 64;" ::"r"(bar_id) : "memory");
             // This warp's reads are done: the accumulator is free for the tile after next.
             tc_fence_before();
             __syncwarp();

@@ -55,6 +55,34 @@ __device__ __forceinline__ float mx_scale(uint32_t b) {
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
+// Two fp32 values in one register pair: sm_100 adds and multiplies them in one instruction.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair_of(float a, float b) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 halves(f32x2 p) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
 // Eight scaled values to elements, nearest with ties to even: 8 bytes (e4m3)
 // or 4 bytes in .x (e2m1, even columns in the low halves).
 template <int FMT>
@@ -83,24 +111,39 @@ __device__ __forceinline__ uint2 mx_pack8(const float (&v)[8]) {
     return make_uint2(r, 0u);
 }
 
+// The larger magnitude; NaN if one is.
+__device__ __forceinline__ float max_abs(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+    return r;
+}
+
 // A quarter block (8 values) of a lane whose neighbours in its group of four
 // hold the rest of the block: the block's scale byte and this lane's elements.
-// A block that holds an infinity or NaN gets scale 255 and zero elements: it
-// reads back as NaN, so nothing that is not a number passes for one.
+// A lane that is not `real` has zeros, whatever v holds.  A block that holds an
+// infinity or NaN gets scale 255 and zero elements: it reads back as NaN, so
+// nothing that is not a number passes for one.
 template <int FMT>
-__device__ __forceinline__ uint2 mx_quarter(const float (&v)[8], uint32_t &byte) {
-    uint32_t m = 0;
+__device__ __forceinline__ uint2 mx_quarter(const f32x2 (&v)[4], bool real, uint32_t &byte) {
+    float m[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i]));
-    m = max(m, __shfl_xor_sync(MOE_FULL_MASK, m, 1));
-    m = max(m, __shfl_xor_sync(MOE_FULL_MASK, m, 2));
-    byte = mx_scale_byte<FMT>(m);
+    for (int i = 0; i < 4; ++i) m[i] = max_abs(halves(v[i]).x, halves(v[i]).y);
+    float top = max_abs(max_abs(m[0], m[1]), max_abs(m[2], m[3]));
+    if (!real) top = 0.0f;
+    top = max_abs(top, __shfl_xor_sync(MOE_FULL_MASK, top, 1));
+    top = max_abs(top, __shfl_xor_sync(MOE_FULL_MASK, top, 2));
+    byte = mx_scale_byte<FMT>(abs_bits(top));
     const float inv = mx_inverse(byte);
+    const f32x2 inv2 = pair_of(inv, inv);
     float s[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s[i] = v[i] * inv;
+    for (int i = 0; i < 4; ++i) {
+        const float2 p = halves(mul2(v[i], inv2));
+        s[2 * i] = p.x;
+        s[2 * i + 1] = p.y;
+    }
     const uint2 q = mx_pack8<FMT>(s);
-    return byte == 255u ? make_uint2(0u, 0u) : q;
+    return byte == 255u || !real ? make_uint2(0u, 0u) : q;
 }
 
 // The same of 8 bf16 values.  Magnitudes are compared as 16-bit integers, two at a time, and
