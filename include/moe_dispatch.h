@@ -509,7 +509,7 @@ moe_status moe_mx_dequantize(const uint8_t *q, const uint8_t *scales, int64_t ro
  * x, residual, residual_out, y [T][d] bf16; gain [d] bf16; q, scales MX rows of
  * `format`.  residual_out (= h), y and q with scales are nullable, not all of
  * them.  residual_out may be residual or x, y may be x or residual (not both
- * outputs the same).  8 <= d <= 16384, d % 8 == 0, eps >= 0.  The mean is
+ * outputs the same: refused).  8 <= d <= 16384, d % 8 == 0, eps >= 0.  The mean is
  * taken in fp32.  As the formula has it, a NaN makes its whole row of y NaN, an
  * infinity gives NaN in its place and zeros beside it.
  */
@@ -524,6 +524,8 @@ moe_status moe_add_rmsnorm(const moe_bf16_t *x, const moe_bf16_t *residual, cons
  * blocks are ragged: offsets as moe_dispatch writes them (or padded ones; the
  * rows between are rows like any other).  No row outside the blocks is read
  * into a result or written.
+ * The tile shape goes by rows / E: where the rows in use are known to be
+ * fewer than a buffer holds, pass their number.
  * xq, xs: MX rows of d values, `rows` of them; w1, w3 (and their scales): MX
  * rows of d values, [E][F] of them; b1, b3 [E][F] fp32, 16-byte aligned, or
  * NULL; h, h_scales: MX rows of F values, padding written.  Products are

@@ -105,10 +105,10 @@ def product_bound(K, absum):
 
 
 def activate(g, u, oai):
-    if oai:
-        g, u = np.minimum(g, 7.0), np.clip(u, -7.0, 7.0)
-        return g / (1.0 + np.exp(-1.702 * g)) * (u + 1.0)
-    with np.errstate(over="ignore"):
+    with np.errstate(over="ignore"):   # a gate far below zero: its limit, 0
+        if oai:
+            g, u = np.minimum(g, 7.0), np.clip(u, -7.0, 7.0)
+            return g / (1.0 + np.exp(-1.702 * g)) * (u + 1.0)
         return g / (1.0 + np.exp(-g)) * u
 
 

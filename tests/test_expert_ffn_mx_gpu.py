@@ -182,7 +182,8 @@ def test_bad_offsets_are_reported(off):
     assert (h.q == 0xA5).all() and (h.scales == 0xA5).all()
 
 
-def test_not_a_number_stays_in_its_row():
+@pytest.mark.parametrize("act", [SWIGLU, OAI])
+def test_not_a_number_stays_in_its_row(act):
     E, d, F, counts = 2, 256, 64, [20, 21]
     off, offsets = blocks(counts)
     rows = int(off[-1])
@@ -191,7 +192,7 @@ def test_not_a_number_stays_in_its_row():
     x[20, 3] = float("inf")
     w = mx_of(randn((E, F, d), 2, 0.1), E2)
     h = filled((rows,), F, E4)
-    moe.moe_expert_gate_up_mx(mx_of(x, E4), offsets, w, w, h)
+    moe.moe_expert_gate_up_mx(mx_of(x, E4), offsets, w, w, h, act=act)
     nan = (h.scales[:, :2] == 255).any(1).cpu()
     assert nan[7] and nan[20] and nan.sum() == 2
     w2 = mx_of(randn((E, d, F), 3, 0.1), E2)
@@ -199,6 +200,70 @@ def test_not_a_number_stays_in_its_row():
     moe.moe_expert_down_mx(h, offsets, w2, y)
     nan = torch.isnan(y).cpu()
     assert nan[7].all() and nan[20].all() and nan.any(1).sum() == 2
+
+
+@pytest.mark.parametrize("act", [SWIGLU, OAI])
+def test_gates_far_out(act):
+    """Gates and ups far beyond the exponential's range, on both sides: 0, the limit or the
+    product, never NaN."""
+    E, d, F, rows = 1, 32, 32, 16
+    x = torch.zeros((rows, d), device=DEV)
+    x[:, 0] = torch.tensor([0, 1e-3, 1, 20, 90, 130, 300, 1e4, 0, -1e-3, -1, -20, -90, -130, -300, -1e4], device=DEV)
+    w1, w3 = torch.zeros((E, F, d), device=DEV), torch.zeros((E, F, d), device=DEV)
+    w1[:, :, 0] = torch.linspace(0.5, 2, F, device=DEV)
+    w3[:, :, 0] = torch.linspace(-1, 1, F, device=DEV)
+    off, offsets = blocks([rows])
+    xs, m1, m3 = mx_of(x, E4), mx_of(w1, E4), mx_of(w3, E4)
+    h = filled((rows,), F, E4)
+    moe.moe_expert_gate_up_mx(xs, offsets, m1, m3, h, act=act)
+    want, bound = mo.gate_up(f64(xs), f64(m1, 0), f64(m3, 0), 0.0, 0.0, act == OAI, d)
+    assert np.isfinite(want).all()
+    check_h(h, want, bound, slice(0, rows))
+
+
+def test_most_experts():
+    """4096 experts, most of them without a row."""
+    E, d, F = 4096, 64, 32
+    counts = (np.arange(E) % 37 == 5).astype(int) * (1 + np.arange(E) % 3)
+    off, offsets = blocks(counts)
+    rows = int(off[-1])
+    xs = mx_of(randn((rows, d), 1), E4)
+    w1, w2 = mx_of(randn((E, F, d), 2, 0.1), E2), mx_of(randn((E, d, F), 3, 0.1), E2)
+    h, y = filled((rows,), F, E4), torch.empty((rows, d), dtype=torch.bfloat16, device=DEV)
+    st = torch.zeros((1,), dtype=torch.int32, device=DEV)
+    moe.moe_expert_gate_up_mx(xs, offsets, w1, w1, h, d_status=st)
+    moe.moe_expert_down_mx(h, offsets, w2, y, d_status=st)
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    for e in np.nonzero(counts)[0]:
+        at = slice(int(off[e]), int(off[e + 1]))
+        want, bound = mo.gate_up(f64(xs, at), f64(w1, e), f64(w1, e), 0.0, 0.0, False, d)
+        check_h(h, want, bound, at)
+        want, bound = mo.down(f64(h, at), f64(w2, e), 0.0, F)
+        assert (np.abs(y[at].double().cpu().numpy() - want) <= bound).all()
+
+
+def test_rows_past_32_bits():
+    """Results of more than 2^32 bytes: the last rows are right and in their place."""
+    E, d, F = 2, 40, 4104
+    rows = (1 << 20) + 77
+    off, offsets = blocks([5, rows - 5])
+    xs = moe.MxRows(*(torch.zeros_like(t) for t in moe.MxRows.empty((rows,), d, E4)[:2]), d, E4)
+    tail = mx_of(randn((9, d), 1), E4)
+    xs.q[-9:], xs.scales[-9:] = tail.q, tail.scales
+    w1 = mx_of(randn((E, F, d), 2, 0.2), E2)
+    h = moe.MxRows.empty((rows,), F, E4)
+    moe.moe_expert_gate_up_mx(xs, offsets, w1, w1, h)
+    want, bound = mo.gate_up(f64(tail), f64(w1, 1), f64(w1, 1), 0.0, 0.0, False, d)
+    check_h(h, want, bound, slice(rows - 9, rows))
+    assert not h.q[5:rows - 9].any()
+    del h
+    w2 = mx_of(randn((E, F, d), 3, 0.2), E2)          # as a down matrix: d inputs, F outputs
+    y = torch.empty((rows, F), dtype=torch.bfloat16, device=DEV)
+    moe.moe_expert_down_mx(xs, offsets, w2, y)
+    want, bound = mo.down(f64(tail), f64(w2, 1), 0.0, d)
+    assert (np.abs(y[-9:].double().cpu().numpy() - want) <= bound).all()
+    assert not y[5:-9].any()
 
 
 def test_no_rows():

@@ -41,7 +41,7 @@ def test_rows_refusals(lib):
         assert lib.moe_mx_dequantize(q, s, rows, K, fmt, x, None) == want
 
 
-def norm(lib, x=A, r=A, g=A, eps=1e-5, T=4, d=64, h=A, y=A, fmt=0, q=A, s=A):
+def norm(lib, x=A, r=A, g=A, eps=1e-5, T=4, d=64, h=A, y=P(8192), fmt=0, q=A, s=A):
     return lib.moe_add_rmsnorm(x, r, g, eps, T, d, h, y, fmt, q, s, None)
 
 
@@ -50,7 +50,7 @@ def test_norm_refusals(lib):
     for kw in (dict(T=-1), dict(d=12), dict(d=0), dict(eps=-1.0), dict(eps=float("nan")),
                dict(fmt=3), dict(s=None), dict(q=None), dict(x=None), dict(g=None),
                dict(h=None, y=None, q=None, s=None), dict(x=P(4104)), dict(r=P(4104)),
-               dict(g=P(4104)), dict(h=P(4104)), dict(y=P(4104)), dict(q=P(4112)), dict(s=P(4104))):
+               dict(g=P(4104)), dict(y=P(8192), h=P(8192)), dict(h=P(4104)), dict(y=P(4104)), dict(q=P(4112)), dict(s=P(4104))):
         assert norm(lib, **kw) == BAD, kw
     assert norm(lib, d=16392) == BIG
     assert norm(lib, T=1 << 31) == BIG

@@ -172,7 +172,7 @@ extern "C" moe_status moe_add_rmsnorm(const moe_bf16_t *x, const moe_bf16_t *res
     if (q && (!mx_format_ok(format) || !scales)) return MOE_ERR_INVALID_ARG;
     if (!q && scales) return MOE_ERR_INVALID_ARG;
     if (T == 0) return MOE_OK;
-    if (!x || !gain || (!residual_out && !y && !q)) return MOE_ERR_INVALID_ARG;
+    if (!x || !gain || (!residual_out && !y && !q) || (y && y == residual_out)) return MOE_ERR_INVALID_ARG;
     for (const void *p : {(const void *)x, (const void *)residual, (const void *)gain,
                           (const void *)residual_out, (const void *)y})
         if (!aligned16(p)) return MOE_ERR_INVALID_ARG;

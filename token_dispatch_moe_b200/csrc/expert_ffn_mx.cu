@@ -103,6 +103,18 @@ __device__ __forceinline__ f32x2 reciprocal2(f32x2 x) {
     return pair_of(v.x, v.y);
 }
 
+// The clamps keep a NaN (fminf and fmaxf would put the limit in its place).
+__device__ __forceinline__ float at_most(float v, float limit) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(v), "f"(limit));
+    return r;
+}
+__device__ __forceinline__ float at_least(float v, float limit) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(v), "f"(limit));
+    return r;
+}
+
 // g becomes act(g, u); a very negative gate gives 0, its limit.
 __device__ __forceinline__ void activate8(f32x2 (&g)[4], const f32x2 (&u)[4], int act) {
     const f32x2 one = pair_of(1.0f, 1.0f);
@@ -111,9 +123,9 @@ __device__ __forceinline__ void activate8(f32x2 (&g)[4], const f32x2 (&u)[4], in
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const float2 a = halves(g[k]), b = halves(u[k]);
-            const f32x2 gc = pair_of(fminf(a.x, kXOaiLimit), fminf(a.y, kXOaiLimit));
-            const f32x2 uc = pair_of(fminf(fmaxf(b.x, -kXOaiLimit), kXOaiLimit),
-                                     fminf(fmaxf(b.y, -kXOaiLimit), kXOaiLimit));
+            const f32x2 gc = pair_of(at_most(a.x, kXOaiLimit), at_most(a.y, kXOaiLimit));
+            const f32x2 uc = pair_of(at_most(at_least(b.x, -kXOaiLimit), kXOaiLimit),
+                                     at_most(at_least(b.y, -kXOaiLimit), kXOaiLimit));
             const f32x2 rc = reciprocal2(add2(exp_neg(mul2(gc, alpha)), one));
             g[k] = mul2(mul2(gc, rc), add2(uc, one));
         }
