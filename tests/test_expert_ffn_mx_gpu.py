@@ -77,6 +77,11 @@ CASES = [
     ([700, 3, 500], 1288, 96, E4, E4, E4, SWIGLU, False, 0),     # several parts a block
     ([40] * 50, 256, 128, E4, E2, E4, OAI, True, 0),             # more tiles than SMs
     ([90, 11], 2048, 768, E4, E2, E4, SWIGLU, False, 0),         # the qwen3 expert
+    ([30, 35, 31], 264, 72, E4, E2, E4, SWIGLU, True, 0),        # token tiles of 48, one CTA
+    ([64, 50, 78, 81], 264, 72, E2, E2, E4, OAI, False, 2),      # 80, pairs from here
+    ([95, 65, 97, 63], 136, 200, E4, E2, E2, SWIGLU, True, 0),   # 96
+    ([180, 150, 210, 211], 136, 200, E4, E4, E4, OAI, True, 0),  # 208
+    ([350, 300, 1, 0, 1020], 136, 72, E4, E2, E4, SWIGLU, True, 7),  # two parts and more
     ([2, 0, 1, 4] * 32, 72, 40, E4, E2, E4, OAI, True, 0),       # 128 experts of few rows
 ]
 

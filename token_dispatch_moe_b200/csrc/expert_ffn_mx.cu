@@ -32,6 +32,8 @@
 // PAIR: two CTAs on two SMs (cta_group::2) hold one token tile: each has its
 // own 128 weight rows, half of the tokens' rows, and all of the tokens' scales.
 // Every wait is bounded, as in the bf16 kernels.
+#include <math.h>
+
 #include "mx.cuh"
 #include "tc.cuh"
 
@@ -43,6 +45,7 @@ constexpr int kXBK = 128;           // K values of a stage
 constexpr int kXSuper = 4;          // stages that one load of scales covers
 constexpr int kXMaxE = 4096;
 constexpr int kXMaxSmem = 227 * 1024;  // of a CTA on sm_100
+constexpr int kXMaxCap = 224;  // tokens of a tile: two accumulators and the scales fill TMEM
 constexpr int kXMaxStages = 12;
 constexpr int kXBars = 512;  // bytes of barriers, the TMEM address and the tile ring
 constexpr int kXEpiThreads = 256;
@@ -823,27 +826,31 @@ moe_status launch_expert_mx(const uint8_t *xq, const uint8_t *xs, int32_t x_fmt,
     return launch_status();
 }
 
-// Tile shape by the rows an expert has on average.  A wider token tile takes shared memory from
-// the weights in flight; a narrower one cuts more blocks into parts, each of which reads the
-// weights again.  About twice the average is best; pairs of CTAs (half of the tokens' bytes per
-// CTA) from where products count.  Measured with 128 experts of 2880 x 2880, e2m1 weights,
-// gate_up in us, by rows an expert (cap 16, 32, 64; pairs with 64, 128, 224):
-//     8:  189  197  217 |  226  268  301        64:  770  433  320 |  334  269  306
-//    16:  238  201  218 |  230  264  316       128: 1390  748  500 |  491  383  365
-//    32:  389  274  230 |  236  271  312
+// Tile shape by the rows an expert has on average.  The token tile should just hold them, and
+// their spread (1.4 of its standard deviation: routing is near a draw), in as few equal parts
+// as fit: wider, it takes shared memory from the weights in flight and loads tokens that are
+// not there (both boxes are cap rows); narrower, more blocks are cut into parts, each of which
+// reads the weights again.  From 33 rows on pairs of CTAs, each with half of the tokens' bytes.
+// Measured with 128 experts of 2880 x 2880, e2m1 weights, gate_up in us, by rows an expert:
+//    8, 20, 32 (one CTA):  cap 16: 189 289 393,  32: 197 203 261,  48: -   202 211,  64: 217 218 238
+//   40, 64, 80 (pairs):    cap 64: 218 332 365,  80: 225 253 316,  96: 226 259 258, 112: 228 275 256
+//   40, 64, 80 (one CTA):  cap 64: 230 339 409,  80: 233 257 339,  96: 251 290 281
+//  128, 256, 512 (pairs):  cap 128: 424 717 1243,  144: 331 622 1192,  192: 380 686 1184,
+//                          224: 386 724 1215
 template <bool GATE_UP>
 moe_status run_expert_mx(const uint8_t *xq, const uint8_t *xs, int32_t x_fmt, const uint8_t *w0,
                          const uint8_t *w0s, const uint8_t *w1, const uint8_t *w1s, int32_t w_fmt,
                          int32_t K, MxFfnArgs a, moe_stream_t stream) {
     const int64_t share = (a.rows + a.E - 1) / a.E;
+    const double need = (double)share + 1.4 * sqrt((double)share);
+    const double parts = ceil(need / kXMaxCap);
+    a.cap = ((int)ceil(need / parts) + 15) / 16 * 16;
     a.ft = GATE_UP ? 64 : 128;
     if (share <= 32) {
-        a.cap = share <= 8 ? 16 : share <= 16 ? 32 : 64;
         a.slots = 4;
         return launch_expert_mx<GATE_UP, false>(xq, xs, x_fmt, w0, w0s, w1, w1s, w_fmt, K, a,
                                                 stream);
     }
-    a.cap = share <= 96 ? 128 : 224;
     a.slots = 3;
     return launch_expert_mx<GATE_UP, true>(xq, xs, x_fmt, w0, w0s, w1, w1s, w_fmt, K, a, stream);
 }
