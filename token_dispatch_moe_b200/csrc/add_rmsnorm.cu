@@ -10,7 +10,8 @@
 // was fused.  The MX rows are made of the rounded y: the gate and the experts
 // see one and the same row, and the bits are moe_mx_quantize's on y.
 //
-// One pass, bound by memory (9.03 bytes a value with every output): a row's
+// One pass, bound by memory (9.03 bytes a value with every output; 65,536 x
+// 7168: 630 us, 6.7 TB/s; 16,384 x 2048: 48 us, 6.3 TB/s): a row's
 // threads keep it in registers between the sum of squares and the outputs.
 // Rows of more than 1024 values have a block of threads each; narrower ones
 // a warp, or half a warp up to 128 values, 8 or 16 rows a block (65,536 x 128:

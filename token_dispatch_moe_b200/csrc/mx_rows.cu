@@ -6,8 +6,13 @@
 // largest magnitude with two shuffles.  A warp takes kRowUnroll * 32
 // consecutive vectors of the rows laid end to end (quantize: padding
 // included), all its loads issued before the first use, so its scales are 32
-// consecutive bytes: they go out in one store (one byte store a vector
-// row of a warp held quantize at 5.0 TB/s).
+// consecutive bytes and go out in one store.  What bounded quantize was the
+// number of instructions (110 a vector, 80 % of the issue slots busy at 4.1
+// TB/s): element rows follow one another without gaps, so stores need no row
+// arithmetic, nor do loads where K is a multiple of 128; magnitudes are
+// compared and scaled two to a register.  Measured, e2m1: 65,536 x 2048 58 us
+// (5.8 TB/s; 78 before), 368,640 x 2880 493 us (5.4; 551 before) and back
+// 400 us (6.7 TB/s); e4m3 6.1 to 6.4 TB/s.
 #include <cuda_fp16.h>
 
 #include "mx.cuh"
