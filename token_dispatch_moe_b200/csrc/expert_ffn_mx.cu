@@ -21,8 +21,8 @@
 //   warp 3     turns raw scale rows [row][16 bytes] into the tiles that TMEM
 //              wants (32 x 16 bytes, four rows' words side by side)
 //   warp 1     scale tiles to TMEM (tcgen05.cp) and four MMAs for every 128 K values
-//   warp 12    walks the tiles and hands them to the other roles through a ring
-//   warps 4-11 epilogue: TMEM -> shared memory, transposed to token-major; each
+//   warp 16    walks the tiles and hands them to the other roles through a ring
+//   warps 4-15 epilogue: TMEM -> shared memory, transposed to token-major; each
 //              thread then takes 8 features of a token: bias, activation, MX
 //              block (four lanes) or bf16, and one vector store
 // Two accumulators: the epilogue of a tile overlaps the next one's products.
@@ -50,7 +50,7 @@
 namespace moe {
 namespace {
 
-constexpr int kXThreads = 416;
+constexpr int kXThreads = 544;  // 4 warps, 12 of the epilogue (128 .. 511), 1
 constexpr int kXBK = 128;           // K values of a stage
 constexpr int kXSuper = 4;          // stages that one load of scales covers
 constexpr int kXMaxE = 4096;
@@ -58,14 +58,15 @@ constexpr int kXMaxSmem = 227 * 1024;  // of a CTA on sm_100
 constexpr int kXMaxCap = 224;  // tokens of a tile: two accumulators and the scales fill TMEM
 constexpr int kXMaxStages = 12;
 constexpr int kXBars = 512;  // bytes of barriers, the TMEM address and the tile ring
-constexpr int kXEpiThreads = 256;
-constexpr int kXChunk = 64;         // token columns the epilogue turns at a time,
-constexpr int kXChunkHalf = 32;     // half of them by each of a quarter's two warps
+constexpr int kXEpiThreads = 384;
+constexpr int kXParts = 3;          // warps that share a quarter of the TMEM lanes
+constexpr int kXPart = 16;          // token columns of a chunk that each of them takes
+constexpr int kXChunk = kXParts * kXPart;
 // Floats of a staged token: 16-byte aligned, the rows of eight reading lanes on different banks.
-// gate_up: 32 gate and 32 up values, a buffer of 32 tokens for each of the 4 pairs of warps;
-// down: 32 values, a buffer for each of the 8 warps.
+// gate_up: 32 gate and 32 up values, a buffer of 16 tokens for each of the 6 pairs of warps;
+// down: 32 values, a buffer for each of the 12 warps.
 constexpr int kXPitch[2] = {36, 68};
-constexpr int kXStageBytes[2] = {8 * kXChunkHalf * 36 * 4, 4 * kXChunkHalf * 68 * 4};
+constexpr int kXStageBytes[2] = {4 * kXParts * kXPart * 36 * 4, 2 * kXParts * kXPart * 68 * 4};
 constexpr float kXOaiAlpha = 1.702f;
 constexpr float kXOaiLimit = 7.0f;
 
@@ -360,14 +361,14 @@ __global__ void __launch_bounds__(kXThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(tfull_bar(b), 1);
-            mbar_init(tempty_bar(b), 8 * kCtas);  // each CTA's epilogue warps
+            mbar_init(tempty_bar(b), kXEpiThreads / 32 * kCtas);  // each CTA's epilogue warps
         }
         mbar_init(drain_bar, 1);
         for (int i = 0; i < kXTiles; ++i) {
             mbar_init(there_bar + 8u * i, 1);
-            // readers: the two loading threads, the turning warp, the epilogue's eight warps,
-            // and the thread that issues the products
-            mbar_init(taken_bar + 8u * i, rank == 0 ? 12 : 11);
+            // readers: the two loading threads, the turning warp, the epilogue's warps, and in
+            // the leader the thread that issues the products
+            mbar_init(taken_bar + 8u * i, 3 + kXEpiThreads / 32 + (rank == 0 ? 1 : 0));
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -593,7 +594,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
             }
         }
         if (!ok) *abort_v = 1;
-    } else if (warp == 12) {
+    } else if (warp == 16) {
         if (lane == 0) {
             Walk walk(a, off, parts, kCtas, rank);
             Tile w;
@@ -609,19 +610,21 @@ __global__ void __launch_bounds__(kXThreads, 1)
             }
         }
     } else {
-        // Two warps share a quarter of the TMEM lanes, half of a chunk's token columns each.
+        // Three warps share a quarter of the TMEM lanes, a third of a chunk's token columns each
+        // (with two the epilogue's latencies held up tiles of few K blocks: qwen3 gate_up 390
+        // against 376 us, 509 ragged rows' down 108 against 103).
         // gate_up: the 32 gate features of quarter q and the same up features, ft / 32 quarters
         // on, are an MX block; the two warps that hold them meet in a staging buffer of their
         // own.  down: a warp's 32 features are its own affair.
-        const int q = warp & 3, half = (warp - 4) >> 2;
+        const int q = warp & 3, part = (warp - 4) >> 2;
         const int quarters = (GATE_UP ? 2 : 1) * a.ft / 32, up = a.ft / 32;
         const bool works = q < quarters;
         const int duo = GATE_UP ? q % up : q;  // block of 32 features
         const int member = GATE_UP && q >= up ? 1 : 0;
-        const int bar_id = 2 + 2 * duo + half;
+        const int bar_id = 2 + kXParts * duo + part;
         constexpr int kPitch = kXPitch[GATE_UP];
         float *stg = reinterpret_cast<float *>(gbase + a.stg) +
-                     (2 * duo + half) * (kXChunkHalf * kPitch);
+                     (kXParts * duo + part) * (kXPart * kPitch);
         Ring acc;
         const int grp = lane & 3;  // 8 of the block's features
         const int cover = a.f_tiles * kCtas * a.ft;  // features of all tiles, N or a little more
@@ -648,14 +651,12 @@ __global__ void __launch_bounds__(kXThreads, 1)
             if (w.n == 0) break;
             tc_fence_after();
             const uint32_t trow = tmem_base + (uint32_t)(acc.at * a.cap) +
-                                  ((uint32_t)(q * 32) << 16) + (uint32_t)(kXChunkHalf * half);
+                                  ((uint32_t)(q * 32) << 16) + (uint32_t)(kXPart * part);
             const int f = w.f0 + 32 * duo + 8 * grp;
             const bool real_f = f < a.N;
-            const int mine = w.n - kXChunkHalf * half;  // tokens from this half's first on
-            // 32 columns as two loads, so that none reads behind the tile's
-            uint32_t v[2][16];
-            if (works && mine > 0) tmem_ld16_nowait(trow, v[0]);
-            if (works && mine > 16) tmem_ld16_nowait(trow + 16u, v[1]);
+            const int mine = w.n - kXPart * part;  // tokens from this part's first on
+            uint32_t v[kXPart];
+            if (works && mine > 0) tmem_ld16_nowait(trow, v);
             f32x2 b0[4], b1[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) b0[k] = b1[k] = 0ull;
@@ -671,47 +672,41 @@ __global__ void __launch_bounds__(kXThreads, 1)
                 tmem_wait_ld();
                 if (c0 > 0) meet();  // the last chunk has been read
 #pragma unroll
-                for (int i = 0; i < kXChunkHalf; ++i)
-                    stg[i * kPitch + 32 * member + lane] = __uint_as_float(v[i >> 4][i & 15]);
-                if (c0 + kXChunk < mine) {
-                    tmem_ld16_nowait(trow + (uint32_t)(c0 + kXChunk), v[0]);
-                    if (c0 + kXChunk + 16 < mine)
-                        tmem_ld16_nowait(trow + (uint32_t)(c0 + kXChunk + 16), v[1]);
-                }
+                for (int i = 0; i < kXPart; ++i)
+                    stg[i * kPitch + 32 * member + lane] = __uint_as_float(v[i]);
+                if (c0 + kXChunk < mine) tmem_ld16_nowait(trow + (uint32_t)(c0 + kXChunk), v);
                 meet();
-                // 32 tokens, four lanes each: 16 a warp (gate_up) or all of them (down), two
-                // eights at a time
-                const int first = GATE_UP ? 16 * member : 0, tokens = GATE_UP ? 16 : 32;
-                for (int t0 = first; t0 < first + tokens && c0 + t0 < mine; t0 += 16) {
+                // 16 tokens, four lanes each: 8 a warp (gate_up), or both eights (down)
 #pragma unroll
-                    for (int t8 = 0; t8 < 16; t8 += 8) {
-                        const int tok = t0 + t8 + (lane >> 2);
-                        const bool there = c0 + tok < mine;
-                        const int64_t row = (int64_t)w.row0 + kXChunkHalf * half + c0 + tok;
-                        const float *src = stg + tok * kPitch + 8 * grp;
-                        f32x2 o[4];
-                        load8(src, o);
+                for (int i = 0; i < (GATE_UP ? 1 : 2); ++i) {
+                    const int t8 = 8 * (GATE_UP ? member : i);
+                    if (c0 + t8 >= mine) break;
+                    const int tok = t8 + (lane >> 2);
+                    const bool there = c0 + tok < mine;
+                    const int64_t row = (int64_t)w.row0 + kXPart * part + c0 + tok;
+                    const float *src = stg + tok * kPitch + 8 * grp;
+                    f32x2 o[4];
+                    load8(src, o);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) o[k] = add2(o[k], b0[k]);
-                        if (GATE_UP) {
-                            f32x2 u[4];
-                            load8(src + 32, u);
+                    for (int k = 0; k < 4; ++k) o[k] = add2(o[k], b0[k]);
+                    if (GATE_UP) {
+                        f32x2 u[4];
+                        load8(src + 32, u);
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) u[k] = add2(u[k], b1[k]);
-                            activate8(o, u, a.act);
-                            // features behind N are zeros of the row's padding
-                            store_h(a, row, f, o, there, real_f && there);
-                        } else if (there && real_f) {
-                            uint32_t p[4];
+                        for (int k = 0; k < 4; ++k) u[k] = add2(u[k], b1[k]);
+                        activate8(o, u, a.act);
+                        // features behind N are zeros of the row's padding
+                        store_h(a, row, f, o, there, real_f && there);
+                    } else if (there && real_f) {
+                        uint32_t p[4];
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const float2 v2 = halves(o[k]);
-                                const __nv_bfloat162 two = __floats2bfloat162_rn(v2.x, v2.y);
-                                p[k] = *reinterpret_cast<const uint32_t *>(&two);
-                            }
-                            *reinterpret_cast<uint4 *>(a.y + row * a.N + f) =
-                                make_uint4(p[0], p[1], p[2], p[3]);
+                        for (int k = 0; k < 4; ++k) {
+                            const float2 v2 = halves(o[k]);
+                            const __nv_bfloat162 two = __floats2bfloat162_rn(v2.x, v2.y);
+                            p[k] = *reinterpret_cast<const uint32_t *>(&two);
                         }
+                        *reinterpret_cast<uint4 *>(a.y + row * a.N + f) =
+                            make_uint4(p[0], p[1], p[2], p[3]);
                     }
                 }
             }
