@@ -463,19 +463,14 @@ _mx_bytes: dict = {}  # (K, format) -> bytes of a row's elements and scales
 def _need_mx(mx, name, ndim=2):
     """Checks MX rows' tensors; the leading sizes are returned."""
     q, scales, K, fmt = mx
-    if q.dtype is not torch.uint8 or scales.dtype is not torch.uint8:
-        raise TypeError(f"{name} must be {torch.uint8}, got {q.dtype} and {scales.dtype}")
-    dev = _current_device() if q.is_cuda and scales.is_cuda else -1
-    if dev < 0 or q.get_device() != dev or scales.get_device() != dev or \
-            not q.is_contiguous() or not scales.is_contiguous():
-        _need(q, torch.uint8, name)
-        _need(scales, torch.uint8, f"{name} scales")
+    _need(q, torch.uint8, name, ndim)
+    _need(scales, torch.uint8, name, ndim)
     sizes = _mx_bytes.get((K, fmt))
     if sizes is None:
         sizes = _mx_bytes[(K, fmt)] = moe_mx_row_bytes(K, fmt)
-    qs, ss = q.shape, scales.shape
-    lead = qs[:-1]
-    if len(qs) != ndim or qs[-1] != sizes[0] or ss[-1] != sizes[1] or ss[:-1] != lead:
+    *lead, row = q.shape
+    *rows, scale = scales.shape
+    if (row, scale) != sizes or rows != lead:
         raise ValueError(f"{name}: shape mismatch")
     return lead
 
@@ -484,21 +479,22 @@ def moe_mx_quantize(x, out: MxRows, stream=None):
     """out = MX rows of the bf16 rows x [..., K]."""
     lead = _need_mx(out, "out", x.dim())
     _need(x, torch.bfloat16, "x")
-    if x.shape != (*lead, out.K):
+    q, scales, K, fmt = out
+    if x.shape != (*lead, K):
         raise ValueError("shape mismatch")
-    _check(load_library().moe_mx_quantize(_ptr(x), math.prod(lead), out.K, out.format, _ptr(out.q),
-                                          _ptr(out.scales), _stream(stream)), "moe_mx_quantize")
+    _check(load_library().moe_mx_quantize(x.data_ptr(), math.prod(lead), K, fmt, q.data_ptr(),
+                                          scales.data_ptr(), _stream(stream)), "moe_mx_quantize")
 
 
 def moe_mx_dequantize(mx: MxRows, out, stream=None):
     """out [..., K] bf16 = the values of MX rows."""
     lead = _need_mx(mx, "mx", out.dim())
     _need(out, torch.bfloat16, "out")
-    if out.shape != (*lead, mx.K):
+    q, scales, K, fmt = mx
+    if out.shape != (*lead, K):
         raise ValueError("shape mismatch")
-    _check(load_library().moe_mx_dequantize(_ptr(mx.q), _ptr(mx.scales), math.prod(lead), mx.K,
-                                            mx.format, _ptr(out), _stream(stream)),
-           "moe_mx_dequantize")
+    _check(load_library().moe_mx_dequantize(q.data_ptr(), scales.data_ptr(), math.prod(lead), K, fmt,
+                                            out.data_ptr(), _stream(stream)), "moe_mx_dequantize")
 
 
 def moe_add_rmsnorm(x, residual, gain, eps, residual_out=None, y=None, mx: MxRows | None = None,
@@ -512,9 +508,9 @@ def moe_add_rmsnorm(x, residual, gain, eps, residual_out=None, y=None, mx: MxRow
         if t is not None and t.shape != x.shape:
             raise ValueError("shape mismatch")
     T, d = x.shape
-    if gain.shape[0] != d or (mx is not None and (_need_mx(mx, "mx") != (T,) or mx.K != d)):
+    q, scales, K, fmt = mx if mx is not None else (None, None, d, 0)
+    if gain.shape[0] != d or K != d or (mx is not None and _need_mx(mx, "mx")[0] != T):
         raise ValueError("shape mismatch")
-    q, scales, _, fmt = mx if mx is not None else (None, None, d, 0)
     _check(load_library().moe_add_rmsnorm(_ptr(x), _ptr(residual), _ptr(gain), eps, T, d,
                                           _ptr(residual_out), _ptr(y), fmt, _ptr(q), _ptr(scales),
                                           _stream(stream)), "moe_add_rmsnorm")
@@ -526,20 +522,20 @@ def moe_expert_gate_up_mx(xs: MxRows, offsets, w1: MxRows, w3: MxRows, h: MxRows
     offsets (w1, w3: [E, F] rows of d values; xs: [rows] of d values; h: [rows] of F values)."""
     _need(offsets, torch.int32, "offsets", 1)
     (rows,) = _need_mx(xs, "xs")
-    E, F = _need_mx(w1, "w1", 3)
+    E, F = lead = _need_mx(w1, "w1", 3)
     for b, n in ((b1, "b1"), (b3, "b3")):
         _need(b, torch.float32, n, 2)
         if b is not None and b.shape != (E, F):
             raise ValueError("shape mismatch")
     _need(d_status, torch.int32, "d_status")
-    if _need_mx(w3, "w3", 3) != (E, F) or _need_mx(h, "h") != (rows,) or w1.K != xs.K or \
-            w3.K != xs.K or w3.format != w1.format or h.K != F or offsets.shape[0] != E + 1:
+    (xq, xsc, d, xf), (w1q, w1s, d1, wf), (w3q, w3s, d3, wf3), (hq, hsc, width, hf) = xs, w1, w3, h
+    if _need_mx(w3, "w3", 3) != lead or _need_mx(h, "h")[0] != rows or d1 != d or d3 != d or \
+            wf3 != wf or width != F or offsets.shape[0] != E + 1:
         raise ValueError("shape mismatch")
     _check(load_library().moe_expert_gate_up_mx(
-        _ptr(xs.q), _ptr(xs.scales), xs.format, _ptr(offsets), _ptr(w1.q), _ptr(w1.scales),
-        _ptr(w3.q), _ptr(w3.scales), w1.format, _ptr(b1), _ptr(b3), E, xs.K, F, rows, act,
-        _ptr(h.q), _ptr(h.scales), h.format, _ptr(d_status), _stream(stream)),
-        "moe_expert_gate_up_mx")
+        xq.data_ptr(), xsc.data_ptr(), xf, offsets.data_ptr(), w1q.data_ptr(), w1s.data_ptr(),
+        w3q.data_ptr(), w3s.data_ptr(), wf, _ptr(b1), _ptr(b3), E, d, F, rows, act, hq.data_ptr(),
+        hsc.data_ptr(), hf, _ptr(d_status), _stream(stream)), "moe_expert_gate_up_mx")
 
 
 def moe_expert_down_mx(h: MxRows, offsets, w2: MxRows, y, b2=None, d_status=None, stream=None):
@@ -551,12 +547,14 @@ def moe_expert_down_mx(h: MxRows, offsets, w2: MxRows, y, b2=None, d_status=None
     _need(d_status, torch.int32, "d_status")
     (rows,) = _need_mx(h, "h")
     E, d = _need_mx(w2, "w2", 3)
-    if w2.K != h.K or y.shape != (rows, d) or offsets.shape[0] != E + 1 or \
+    (hq, hsc, F, hf), (wq, wsc, width, wf) = h, w2
+    if width != F or y.shape != (rows, d) or offsets.shape[0] != E + 1 or \
             (b2 is not None and b2.shape != (E, d)):
         raise ValueError("shape mismatch")
     _check(load_library().moe_expert_down_mx(
-        _ptr(h.q), _ptr(h.scales), h.format, _ptr(offsets), _ptr(w2.q), _ptr(w2.scales), w2.format,
-        _ptr(b2), E, d, h.K, rows, _ptr(y), _ptr(d_status), _stream(stream)), "moe_expert_down_mx")
+        hq.data_ptr(), hsc.data_ptr(), hf, offsets.data_ptr(), wq.data_ptr(), wsc.data_ptr(), wf,
+        _ptr(b2), E, d, F, rows, y.data_ptr(), _ptr(d_status), _stream(stream)),
+        "moe_expert_down_mx")
 
 
 def moe_wait_probe(limit_ns: int, d_status, d_outcome=None, stream=None):

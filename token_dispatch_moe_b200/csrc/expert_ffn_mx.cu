@@ -34,7 +34,7 @@
 // Every wait is bounded, as in the bf16 kernels.
 //
 // What bounds it.  Few rows: the weights' bytes (128 experts of 2880 x 2880, 64
-// tokens of 4 slots: gate_up 165 us for 0.98 GB, 6.0 TB/s).  Inside an SM a K
+// tokens of 4 slots: gate_up 158 to 164 us for 0.98 GB, 6.0 to 6.2 TB/s).  Inside an SM a K
 // block costs 32 KB of shared memory traffic (16 KB of widened weights written
 // and read), 256 clocks at least and 290 measured, under HBM's share.  Many
 // rows: tensor pipe, L2 reads and the power cap together (131,072 rows: gate_up
@@ -851,12 +851,10 @@ moe_status run_expert_mx(const uint8_t *xq, const uint8_t *xs, int32_t x_fmt, co
     const double parts = ceil(need / kXMaxCap);
     a.cap = ((int)ceil(need / parts) + 15) / 16 * 16;
     a.ft = GATE_UP ? 64 : 128;
-    if (share <= 32) {
-        a.slots = 4;
+    a.slots = 4;
+    if (share <= 32)
         return launch_expert_mx<GATE_UP, false>(xq, xs, x_fmt, w0, w0s, w1, w1s, w_fmt, K, a,
                                                 stream);
-    }
-    a.slots = 3;
     return launch_expert_mx<GATE_UP, true>(xq, xs, x_fmt, w0, w0s, w1, w1s, w_fmt, K, a, stream);
 }
 
