@@ -1,0 +1,65 @@
+"""moe_expert_gate_up_mx and moe_expert_down_mx launched close together: a CTA pair's end, beside
+kernels that take over its shared memory, and calls from several host threads."""
+import pytest
+import torch
+
+import token_dispatch_moe_b200 as moe
+from test_expert_ffn_mx_gpu import DEV, E2, E4, blocks, f64, mx_of, randn
+import mx_oracle as mo
+import numpy as np
+
+pytestmark = pytest.mark.gpu
+
+
+class Call:
+    """The two products over one routing: run() launches both; check() compares with the first
+    run's bits, and once with the definition."""
+
+    def __init__(self, counts, d, F, seed):
+        E = len(counts)
+        self.d, self.F, self.first = d, F, None
+        self.off, self.offsets = blocks(counts)
+        rows = int(self.off[-1])
+        self.xs = mx_of(randn((rows, d), seed), E4)
+        self.w1 = mx_of(randn((E, F, d), seed + 1, d ** -0.5), E2)
+        self.w2 = mx_of(randn((E, d, F), seed + 2, F ** -0.5), E2)
+        self.h = moe.MxRows.empty((rows,), F, E4)
+        self.y = torch.empty((rows, d), dtype=torch.bfloat16, device=DEV)
+        self.st = torch.zeros((1,), dtype=torch.int32, device=DEV)
+
+    def run(self, stream=None):
+        moe.moe_expert_gate_up_mx(self.xs, self.offsets, self.w1, self.w1, self.h, d_status=self.st,
+                                  stream=stream)
+        moe.moe_expert_down_mx(self.h, self.offsets, self.w2, self.y, d_status=self.st, stream=stream)
+
+    def check(self):
+        assert self.st.item() == 0
+        got = (self.h.q.clone(), self.h.scales.clone(), self.y.clone())
+        if self.first is None:
+            for e in range(len(self.off) - 1):
+                at = slice(int(self.off[e]), int(self.off[e + 1]))
+                if at.start < at.stop:
+                    want, bound = mo.down(f64(self.h, at), f64(self.w2, e), 0.0, self.F)
+                    assert (np.abs(self.y[at].double().cpu().numpy() - want) <= bound).all()
+            self.first = got
+        for a, b in zip(got, self.first):
+            assert torch.equal(a, b)
+        for t in (self.h.q, self.h.scales, self.y):
+            t.fill_(0)
+
+
+def test_pairs_close_together():
+    """Many short launches of CTA pairs, of different shapes (their barriers lie at different
+    places), with single-CTA launches and the row kernels between: every launch's bits are the
+    first one's."""
+    calls = [Call([90, 11, 70], 256, 264, 1),        # pairs
+             Call([40] * 5, 128, 72, 11),            # pairs, fewer tokens a tile
+             Call([3, 8, 1], 384, 136, 21),          # one CTA a tile
+             Call([700, 3, 500], 136, 392, 31)]      # pairs, several tiles a block
+    for turn in range(40):
+        for _ in range(5):
+            for c in calls:
+                c.run()
+        torch.cuda.synchronize()
+        for c in calls:
+            c.check()

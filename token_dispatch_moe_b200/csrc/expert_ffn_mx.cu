@@ -455,12 +455,20 @@ __global__ void __launch_bounds__(kXThreads, 1)
                 }
             }
             if (!ok) *abort_v = 1;
-            // Drain (the leader's barriers count both CTAs' bytes): the last loads into every
-            // stage have landed before the CTAs exit.
-            for (uint32_t i = 0, n = rank == 0 ? min(filled, (uint32_t)S) : 0u; i < n; ++i) {
+            // Drain: the last loads into every stage have landed (the leader's barriers count
+            // both CTAs' bytes), and the arrivals that tell of their last use, before the CTAs
+            // exit.  In a pair those come from the leader's commits, over the cluster's network.
+            for (uint32_t i = 0, n = min(filled, (uint32_t)S); i < n; ++i) {
                 st.back(S);
-                if (!mbar_wait(full_bar(st.at), st.pass, a.status)) break;
+                if (rank == 0 && !mbar_wait(full_bar(st.at), st.pass, a.status)) {
+                    *abort_v = 1;
+                    break;
+                }
+                if (!*abort_v && !mbar_wait(empty_bar(st.at), st.pass, a.status)) *abort_v = 1;
             }
+            // The leader's last commit arrives here too, on every path, after a wait that gave
+            // up as well: so the limit is above that of the leader's own waits.
+            if (PAIR && rank != 0) mbar_wait_for(drain_bar, 0u, a.status, 3 * kWaitLimitNs);
         }
     } else if (warp == 1) {
         if (rank == 0 && elect_one()) {
@@ -556,9 +564,13 @@ __global__ void __launch_bounds__(kXThreads, 1)
                 }
             }
             if (!ok) *abort_v = 1;
-            for (uint32_t i = 0, n = min(filled, (uint32_t)R); i < n; ++i) {
+            for (uint32_t i = 0, n = min(filled, (uint32_t)R); i < n; ++i) {  // as warp 0 does
                 sf.back(R);
-                if (!mbar_wait(raw_bar(sf.at), sf.pass, a.status)) break;
+                if (!mbar_wait(raw_bar(sf.at), sf.pass, a.status)) {
+                    *abort_v = 1;
+                    break;
+                }
+                if (!*abort_v && !mbar_wait(free_bar(sf.at), sf.pass, a.status)) *abort_v = 1;
             }
         }
     } else if (warp == 3) {
@@ -738,7 +750,8 @@ __global__ void __launch_bounds__(kXThreads, 1)
 
     tc_fence_before();
     if (PAIR)
-        cluster_sync();  // no CTA leaves while the other may use its memory or barriers
+        cluster_sync();  // with the drains above: no CTA leaves while the other, or a commit of
+                         // the leader's on its way, may use its memory or barriers
     else
         __syncthreads();
     if (warp == 2) {
