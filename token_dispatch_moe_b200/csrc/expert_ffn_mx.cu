@@ -94,12 +94,15 @@ struct MxFfnArgs {
 // e^-x to a few units of fp32, two at a time: 2^t with t = -x log2(e) rounded, times what the
 // rounding of t and of log2(e) lost (to first order).  Without that factor the error grows with
 // |x|, to 1e-6 at |x| = 10: no matter to the value of h, but ten times as many of its roundings
-// (and of its blocks' powers of two) would fall on the other side than the exact sum's.  From
-// x = -200 down the result is infinite.
+// (and of its blocks' powers of two) would fall on the other side than the exact sum's.  x is
+// held between -200 and 200, where the result is infinite and 0: past 2.36e38 the product with
+// log2(e) would overflow.  BELOW: x is at most 200 by itself.
+template <bool BELOW>
 __device__ __forceinline__ f32x2 exp_neg(f32x2 x) {
-    constexpr float kL = 1.44269504f, kLLow = 1.92596299e-8f, kLn2 = 0.693147181f;
+    constexpr float kL = 1.44269504f, kLLow = 1.92596299e-8f, kLn2 = 0.693147181f, kFar = 200.0f;
     const float2 v = halves(x);
-    const float a = fmaxf(v.x, -200.0f), b = fmaxf(v.y, -200.0f);
+    const float a = fmaxf(BELOW ? v.x : fminf(v.x, kFar), -kFar);
+    const float b = fmaxf(BELOW ? v.y : fminf(v.y, kFar), -kFar);
     const float ta = -a * kL, tb = -b * kL;
     const f32x2 lost = fma2(pair_of(a, b), pair_of(-kLLow, -kLLow),
                             pair_of(fmaf(-a, kL, -ta), fmaf(-b, kL, -tb)));
@@ -140,13 +143,13 @@ __device__ __forceinline__ void activate8(f32x2 (&g)[4], const f32x2 (&u)[4], in
             const f32x2 gc = pair_of(at_most(a.x, kXOaiLimit), at_most(a.y, kXOaiLimit));
             const f32x2 uc = pair_of(at_most(at_least(b.x, -kXOaiLimit), kXOaiLimit),
                                      at_most(at_least(b.y, -kXOaiLimit), kXOaiLimit));
-            const f32x2 rc = reciprocal2(add2(exp_neg(mul2(gc, alpha)), one));
+            const f32x2 rc = reciprocal2(add2(exp_neg<true>(mul2(gc, alpha)), one));
             g[k] = mul2(mul2(gc, rc), add2(uc, one));
         }
     } else {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            g[k] = mul2(mul2(g[k], reciprocal2(add2(exp_neg(g[k]), one))), u[k]);
+            g[k] = mul2(mul2(g[k], reciprocal2(add2(exp_neg<false>(g[k]), one))), u[k]);
     }
 }
 
