@@ -1,5 +1,7 @@
 """moe_expert_gate_up_mx and moe_expert_down_mx launched close together: a CTA pair's end, beside
 kernels that take over its shared memory, and calls from several host threads."""
+import threading
+
 import pytest
 import torch
 
@@ -63,3 +65,47 @@ def test_pairs_close_together():
         torch.cuda.synchronize()
         for c in calls:
             c.check()
+
+
+@pytest.mark.parametrize("shapes", [
+    [([3, 8, 1], 384, 136), ([1, 2] * 300, 64, 32), ([30, 31], 136, 72), ([12] * 64, 128, 64)],
+    [([90, 11, 70], 256, 264), ([40] * 100, 128, 72), ([700, 3, 500], 136, 392), ([64] * 9, 64, 32)],
+], ids=["one CTA", "pairs"])
+def test_calls_of_several_host_threads(shapes):
+    """Four host threads, each with its own stream, sizes and expert count (so its own shared
+    memory), launch at the same time (ctypes lets the interpreter's lock go during a call): no
+    call fails, and the bits are those of one thread alone."""
+    calls = [Call(*s, seed=5 + 10 * i) for i, s in enumerate(shapes)]
+    for c in calls:
+        c.run()
+    torch.cuda.synchronize()
+    for c in calls:
+        c.check()
+    failed = launch_together([lambda s, c=c: c.run(s) for c in calls], 1500)
+    assert not failed, failed[0]
+    for c in calls:
+        c.check()
+
+
+def launch_together(steps, times):
+    """step(stream) for each of steps, `times` times in a thread of its own; the errors."""
+    failed, start = [], threading.Barrier(len(steps))
+
+    def work(step):
+        stream = torch.cuda.Stream()
+        torch.zeros((1,), device=DEV)  # the thread's context is set up
+        start.wait()
+        try:
+            for _ in range(times):
+                step(stream)
+        except moe.MoeError as e:
+            failed.append(e)
+        stream.synchronize()
+
+    threads = [threading.Thread(target=work, args=(s,)) for s in steps]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    return failed

@@ -29,6 +29,19 @@ inline int sm_count() {
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Lets launches of fn on the current device ask for up to `most` bytes of dynamic shared
+// memory.  The limit belongs to the function, not to a launch: a launcher passes the same
+// `most` in every call, whatever the call itself needs, or host threads that launch at the
+// same time would lower it under one another.
+template <typename Fn>
+inline moe_status allow_smem(Fn *fn, size_t most) {
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) ==
+        cudaSuccess)
+        return MOE_OK;
+    cudaGetLastError();
+    return MOE_ERR_CUDA;
+}
+
 // Programmatic dependent launch: the kernel may be scheduled while the kernel
 // before it on the stream finishes.  Such a kernel calls griddep_wait() before
 // it touches global memory (that wait returns once the previous grid has

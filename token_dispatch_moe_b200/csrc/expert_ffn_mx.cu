@@ -54,7 +54,7 @@ constexpr int kXThreads = 544;  // 4 warps, 12 of the epilogue (128 .. 511), 1
 constexpr int kXBK = 128;           // K values of a stage
 constexpr int kXSuper = 4;          // stages that one load of scales covers
 constexpr int kXMaxE = 4096;
-constexpr int kXMaxSmem = 227 * 1024;  // of a CTA on sm_100
+constexpr int kXMaxDynamic = 227 * 1024 - 64;  // of a CTA on sm_100, without the static part
 constexpr int kXMaxCap = 224;  // tokens of a tile: two accumulators and the scales fill TMEM
 constexpr int kXMaxStages = 12;
 constexpr int kXBars = 512;  // bytes of barriers, the TMEM address and the tile ring
@@ -794,10 +794,10 @@ moe_status launch_expert_mx(const uint8_t *xq, const uint8_t *xs, int32_t x_fmt,
     a.tmem_cols = cols;
     const uint32_t stg = kXStageBytes[GATE_UP], bars = kXBars;
     const uint32_t tables = ((uint32_t)(2 * (a.E + 1)) * 4u + 15u) / 16u * 16u;
-    // alignment slack, static shared memory; MMAs read 128 weight rows where a tile has fewer:
-    // what lies behind the stages is large enough for that
-    const int64_t rest = (int64_t)kXMaxSmem - 1024 - 64 - stg - bars - tables -
-                         (int64_t)a.slots * a.slot_bytes;
+    // 1024: alignment slack; MMAs read 128 weight rows where a tile has fewer: what lies behind
+    // the stages is large enough for that
+    const int64_t rest =
+        (int64_t)kXMaxDynamic - 1024 - stg - bars - tables - (int64_t)a.slots * a.slot_bytes;
     int64_t stages = rest / a.stage_bytes;
     if (stages > kXMaxStages) stages = kXMaxStages;
     if (stages < 2) return MOE_ERR_UNSUPPORTED;
@@ -820,12 +820,7 @@ moe_status launch_expert_mx(const uint8_t *xq, const uint8_t *xs, int32_t x_fmt,
     if (GATE_UP && (!make_mx_map(&mw1, w1, wrows, Kp, w4, a.ft) ||
                     !make_byte_map(&mw1s, w1s, wrows, sp, a.ft)))
         return MOE_ERR_CUDA;
-    if (cudaFuncSetAttribute(expert_mx_kernel<GATE_UP, PAIR>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-        cudaSuccess) {
-        cudaGetLastError();
-        return MOE_ERR_CUDA;
-    }
+    if (allow_smem(expert_mx_kernel<GATE_UP, PAIR>, kXMaxDynamic) != MOE_OK) return MOE_ERR_CUDA;
     // Never more CTAs than the most tiles these rows can make.
     const int64_t parts = a.rows / a.cap + (a.rows < a.E ? a.rows : a.E);
     const int64_t most = parts * a.f_tiles, slots = sm_count() / kCtas;
