@@ -32,7 +32,9 @@ inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 
 // Lets launches of fn on the current device ask for up to `most` bytes of dynamic shared
 // memory.  The limit belongs to the function, not to a launch: a launcher passes the same
 // `most` in every call, whatever the call itself needs, or host threads that launch at the
-// same time would lower it under one another.
+// same time would lower it under one another.  A launcher calls this before it encodes a
+// tensor map: the map takes a current context, and a host thread's first runtime call that
+// needs the device sets it.
 template <typename Fn>
 inline moe_status allow_smem(Fn *fn, size_t most) {
     if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) ==

@@ -355,16 +355,17 @@ moe_status launch_expert_gemm(const moe_bf16_t *A, const moe_bf16_t *B0, const m
     if (stages < 2) return MOE_ERR_UNSUPPORTED;
     a.stages = stages;
     const size_t smem = (size_t)stages * a.stage_bytes + overhead;
-    CUtensorMap ma, mb0, mb1;
-    const int64_t brows = (int64_t)a.E * a.N;
-    if (!make_map(&ma, A, rows, K, kFBM) || !make_map(&mb0, B0, brows, K, a.BN) ||
-        !make_map(&mb1, GATE_UP ? B1 : B0, brows, K, a.BN))
-        return MOE_ERR_CUDA;
+    // before the maps: it sets the host thread's context, which they need
     if (cudaFuncSetAttribute(expert_gemm_kernel<GATE_UP>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
         cudaGetLastError();
         return MOE_ERR_CUDA;
     }
+    CUtensorMap ma, mb0, mb1;
+    const int64_t brows = (int64_t)a.E * a.N;
+    if (!make_map(&ma, A, rows, K, kFBM) || !make_map(&mb0, B0, brows, K, a.BN) ||
+        !make_map(&mb1, GATE_UP ? B1 : B0, brows, K, a.BN))
+        return MOE_ERR_CUDA;
     // Persistent: kFfnCtasPerSm CTAs per SM, never more than the largest tile count.
     const int64_t most = (int64_t)(a.N / a.BN) * ((rows + kFBM - 1) / kFBM);
     const int64_t slots = (int64_t)sm_count() * kFfnCtasPerSm;

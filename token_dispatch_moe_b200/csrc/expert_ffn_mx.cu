@@ -807,6 +807,7 @@ moe_status launch_expert_mx(const uint8_t *xq, const uint8_t *xs, int32_t x_fmt,
     a.bars = a.stg + stg;
     a.tables = a.bars + bars;
     const size_t smem = 1024 + (size_t)a.tables + tables;
+    if (allow_smem(expert_mx_kernel<GATE_UP, PAIR>, kXMaxDynamic) != MOE_OK) return MOE_ERR_CUDA;
     CUtensorMap mw0, mw1, mw0s, mw1s, mx, mxs;
     const int64_t wrows = (int64_t)a.E * a.N;
     const int64_t Kp = mx_padded(K), sp = mx_scale_bytes(K);
@@ -820,7 +821,6 @@ moe_status launch_expert_mx(const uint8_t *xq, const uint8_t *xs, int32_t x_fmt,
     if (GATE_UP && (!make_mx_map(&mw1, w1, wrows, Kp, w4, a.ft) ||
                     !make_byte_map(&mw1s, w1s, wrows, sp, a.ft)))
         return MOE_ERR_CUDA;
-    if (allow_smem(expert_mx_kernel<GATE_UP, PAIR>, kXMaxDynamic) != MOE_OK) return MOE_ERR_CUDA;
     // Never more CTAs than the most tiles these rows can make.
     const int64_t parts = a.rows / a.cap + (a.rows < a.E ? a.rows : a.E);
     const int64_t most = parts * a.f_tiles, slots = sm_count() / kCtas;
