@@ -86,3 +86,65 @@ def test_first_call_of_a_thread(name, own_stream):
     in_new_thread(lambda: call(stream))
     for a, b in zip(outs, want):
         assert torch.equal(a, b)
+
+
+def sized(kind, i):
+    """(call(stream), outputs) of one entry point at its i-th size: the sizes ask for different
+    amounts of shared memory."""
+    g = torch.Generator(device=DEV).manual_seed(10 + i)
+    rand = lambda *s: torch.randn(s, generator=g, device=DEV)
+    bf = lambda *s: rand(*s).to(torch.bfloat16)
+    n = (8, 64, 200, 512)[i]
+    if kind == "gate_gemm":
+        x, w, out = bf(300, 256), bf(n, 256), torch.zeros((300, n), device=DEV)
+        return lambda s: moe.moe_gate_gemm(x, w, out, stream=s), [out]
+    if kind in ("expert_gate_up", "expert_down"):
+        N, rows = (16, 96, 128, 160)[i], 256
+        offsets = torch.tensor([0] * (n // 2) + [rows] * (n // 2 + 1), dtype=torch.int32, device=DEV)
+        if kind == "expert_gate_up":
+            x, w, out = bf(rows, 64), bf(n, N, 64), torch.zeros((rows, N), dtype=torch.bfloat16, device=DEV)
+            return lambda s: moe.moe_expert_gate_up(x, offsets, w, w, out, stream=s), [out]
+        x, w, out = bf(rows, 64), bf(n, N, 64), torch.zeros((rows, N), dtype=torch.bfloat16, device=DEV)
+        return lambda s: moe.moe_expert_down(x, offsets, w, out, stream=s), [out]
+    k_max = 4 if kind == "route" else 12
+    E_ = (32, 64, 256, 512)[i] if kind == "route" else (36, 128, 260, 512)[i]
+    T_ = (50, 3000, 700, 9000)[i]
+    logits, ids = rand(T_, E_), torch.zeros((T_, k_max), dtype=torch.int32, device=DEV)
+    tw = torch.zeros((T_, k_max), device=DEV)
+    params = moe.RouteParams.make(E_, k_max, moe.SCORE_SOFTMAX, 1, 1, 1, True, 1.0)
+    return lambda s: moe.moe_route(logits, None, None, params, ids, tw, stream=s), [ids, tw]
+
+
+@pytest.mark.parametrize("kind", ["gate_gemm", "expert_gate_up", "expert_down", "route", "route_k12"])
+def test_sizes_of_several_threads_at_once(kind):
+    """Four host threads launch one entry point at sizes of different shared memory: no call
+    fails, and the bits are those of one thread alone."""
+    all_ = [sized(kind, i) for i in range(4)]
+    want = []
+    for call, outs in all_:
+        call(None)
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in outs])
+    errors, start = [], threading.Barrier(4)
+
+    def work(call):
+        stream = torch.cuda.Stream()
+        torch.zeros((1,), device=DEV)
+        start.wait()
+        try:
+            for _ in range(2000):
+                call(stream)
+        except moe.MoeError as e:
+            errors.append(e)
+        stream.synchronize()
+
+    threads = [threading.Thread(target=work, args=(call,)) for call, _ in all_]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors[0]
+    torch.cuda.synchronize()
+    for (_, outs), w in zip(all_, want):
+        for a, b in zip(outs, w):
+            assert torch.equal(a, b)

@@ -355,12 +355,7 @@ moe_status launch_expert_gemm(const moe_bf16_t *A, const moe_bf16_t *B0, const m
     if (stages < 2) return MOE_ERR_UNSUPPORTED;
     a.stages = stages;
     const size_t smem = (size_t)stages * a.stage_bytes + overhead;
-    // before the maps: it sets the host thread's context, which they need
-    if (cudaFuncSetAttribute(expert_gemm_kernel<GATE_UP>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
-        cudaGetLastError();
-        return MOE_ERR_CUDA;
-    }
+    if (allow_smem(expert_gemm_kernel<GATE_UP>, kMaxDynamicSmem) != MOE_OK) return MOE_ERR_CUDA;
     CUtensorMap ma, mb0, mb1;
     const int64_t brows = (int64_t)a.E * a.N;
     if (!make_map(&ma, A, rows, K, kFBM) || !make_map(&mb0, B0, brows, K, a.BN) ||

@@ -631,12 +631,7 @@ moe_status plan_gemm(int64_t T, int32_t d, int32_t E, size_t epi_bytes, GemmArgs
 template <int MODE, int P, bool MONO, bool GROUPED, int NC>
 moe_status launch_gate_nc(const moe_bf16_t *x, const moe_bf16_t *w, const GemmArgs &a,
                        const FusedArgs &f, size_t smem, int32_t d, moe_stream_t stream) {
-    // before the maps: it sets the host thread's context, which they need
-    if (cudaFuncSetAttribute(gate_kernel<MODE, P, MONO, GROUPED, NC>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
-        cudaGetLastError();
-        return MOE_ERR_CUDA;
-    }
+    if (allow_smem(gate_kernel<MODE, P, MONO, GROUPED, NC>, kMaxDynamicSmem) != MOE_OK) return MOE_ERR_CUDA;
     CUtensorMap mx, mw;
     if (!make_map(&mx, x, a.T, d, kBM) || !make_map(&mw, w, a.E, d, a.BN / 2)) return MOE_ERR_CUDA;
     // One pair of CTAs (a cluster of two) per 256 rows.

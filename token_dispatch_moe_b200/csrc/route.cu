@@ -43,6 +43,14 @@ namespace {
 constexpr int kRouteWarps = 8;  // warps per block
 constexpr int kMaxE = kRouteMaxE;
 constexpr int kStages = 3;
+// Most dynamic shared memory of a block: three stages of at most 4096 logits (or 8 rows, no more
+// at 512 experts) and 256 k's, and a row's keys for each warp.
+constexpr size_t kRouteMaxSmem =
+    (size_t)kStages * (4096 + 256) * 4 + kStages * 8 + (size_t)kRouteWarps * kMaxE * 4;
+// ... of the quad kernel: 32 chunks of 512 bytes a warp, 512 biases, group scores, a row's keys.
+constexpr size_t kQuadMaxSmem = (size_t)kQuadWarps * 32 * 512 + 512 * 4 +
+                                (size_t)(kQuadThreads / 4) * kQuadGroupStride * 4 +
+                                (size_t)kQuadWarps * kRouteMaxE * 4;
 
 // ---------------------------------------------------------------- helpers --
 // Copies `bytes` (a multiple of 16, may be 0) from global src to shared dst;
@@ -345,11 +353,7 @@ extern "C" moe_status moe_route(const float *logits, const float *bias, const in
         const bool fixed_words = a.keys_from_scores && (p->score == MOE_SCORE_SIGMOID ||
                                                          p->score == MOE_SCORE_SOFTMAX);
         void *fn = fixed_words ? route_quad_fn_fixed(P, a.nch) : route_quad_fn_float(P, a.nch);
-        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-            cudaSuccess) {
-            cudaGetLastError();
-            return MOE_ERR_CUDA;
-        }
+        if (allow_smem(fn, kQuadMaxSmem) != MOE_OK) return MOE_ERR_CUDA;
         int per_sm = 0;
         if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, kQuadThreads, smem) !=
                 cudaSuccess ||
@@ -389,11 +393,7 @@ extern "C" moe_status moe_route(const float *logits, const float *bias, const in
     const size_t smem = (size_t)kStages * R * E * sizeof(float) + (size_t)kStages * R * sizeof(int32_t) +
                         kStages * sizeof(uint64_t) +
                         (a.group_mode == 3 ? (size_t)kRouteWarps * kMaxE * sizeof(float) : 0);
-    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-        cudaSuccess) {
-        cudaGetLastError();
-        return MOE_ERR_CUDA;
-    }
+    if (allow_smem(fn, kRouteMaxSmem) != MOE_OK) return MOE_ERR_CUDA;
     int per_sm = 0;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, kRouteWarps * 32, smem) !=
             cudaSuccess ||

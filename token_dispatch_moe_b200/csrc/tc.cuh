@@ -11,6 +11,9 @@
 namespace moe {
 
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // bound of every mbarrier wait
+// Most dynamic shared memory of a CTA on sm_100, beside the 1 KB that a kernel's own static
+// variables take where its shared memory is aligned to 1024 bytes.
+constexpr size_t kMaxDynamicSmem = 226 * 1024;
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
