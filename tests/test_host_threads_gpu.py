@@ -115,36 +115,50 @@ def sized(kind, i):
     return lambda s: moe.moe_route(logits, None, None, params, ids, tw, stream=s), [ids, tw]
 
 
-@pytest.mark.parametrize("kind", ["gate_gemm", "expert_gate_up", "expert_down", "route", "route_k12"])
-def test_sizes_of_several_threads_at_once(kind):
-    """Four host threads launch one entry point at sizes of different shared memory: no call
-    fails, and the bits are those of one thread alone."""
-    all_ = [sized(kind, i) for i in range(4)]
-    want = []
-    for call, outs in all_:
-        call(None)
-        torch.cuda.synchronize()
-        want.append([t.clone() for t in outs])
-    errors, start = [], threading.Barrier(4)
+class Recorder:
+    """The library's handle, keeping the last call: (function, arguments)."""
 
-    def work(call):
+    def __init__(self, lib):
+        self.lib, self.last = lib, None
+
+    def __getattr__(self, name):
+        fn = getattr(self.lib, name)
+
+        def call(*args):
+            self.last = fn, args
+            return fn(*args)
+
+        return call
+
+
+@pytest.mark.parametrize("kind", ["gate_gemm", "expert_gate_up", "expert_down", "route", "route_k12"])
+def test_sizes_of_several_threads_at_once(kind, monkeypatch):
+    """Four host threads launch one entry point at sizes of different shared memory, with nothing
+    but the C call in their loops: no call fails, and the bits are those of one thread alone."""
+    recorder = Recorder(moe.load_library())
+    monkeypatch.setattr(moe, "_lib", recorder)
+    jobs = []
+    for i in range(4):
+        call, outs = sized(kind, i)
         stream = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        call(stream)
+        torch.cuda.synchronize()
+        jobs.append((*recorder.last, outs, [t.clone() for t in outs], stream, call))  # call: the inputs
+    failed, start = [], threading.Barrier(4)
+
+    def work(fn, args):
         torch.zeros((1,), device=DEV)
         start.wait()
-        try:
-            for _ in range(2000):
-                call(stream)
-        except moe.MoeError as e:
-            errors.append(e)
-        stream.synchronize()
+        failed.extend(s for s in (fn(*args) for _ in range(20000)) if s != moe.MOE_OK)
 
-    threads = [threading.Thread(target=work, args=(call,)) for call, _ in all_]
+    threads = [threading.Thread(target=work, args=job[:2]) for job in jobs]
     for t in threads:
         t.start()
     for t in threads:
         t.join()
-    assert not errors, errors[0]
     torch.cuda.synchronize()
-    for (_, outs), w in zip(all_, want):
-        for a, b in zip(outs, w):
+    assert not failed, failed[:5]
+    for _, _, outs, want, *_ in jobs:
+        for a, b in zip(outs, want):
             assert torch.equal(a, b)
