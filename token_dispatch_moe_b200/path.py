@@ -66,7 +66,7 @@ class RouterDispatch:
                     if wl.combine else None)
         self.status = torch.zeros((1,), **i32)
         self.h = self.y = None
-        if wl.ffn_dim and wl.pad % 128 == 0:  # the experts' FFN can run on these blocks
+        if mx is None and wl.ffn_dim and wl.pad % 128 == 0:  # the experts' FFN can run on these blocks
             self.h = torch.empty((max(self.expert_rows, 1), wl.ffn_dim), dtype=torch.bfloat16,
                                  device=device)
             self.y = torch.empty((max(self.expert_rows, 1), wl.d), dtype=torch.bfloat16,
@@ -83,6 +83,11 @@ class RouterDispatch:
         if wl.hash_vocab:
             self.hash_ids = torch.empty((T, k), **i32)
             self.hash_w = torch.empty((T, k), dtype=torch.float32, device=device)
+
+    def _rows_are(self, mx: bool, step: str):
+        if (self.mx is not None) != mx:
+            raise ValueError(f"{step}: this path's rows are {'bf16' if mx else 'MX'} "
+                             f"(RouterDispatch mx={self.mx})")
 
     # Individual steps (each one C-ABI call) -----------------------------------
     def gate(self, x, w, stream=None):
@@ -112,37 +117,44 @@ class RouterDispatch:
                          self.dest_pos, self.workspace, self.status, stream)
 
     def permute(self, x, stream=None):
+        self._rows_are(False, "permute")
         moe_permute(x, self.dest_pos, self.xs, stream)
 
     def combine(self, y, shared=None, stream=None):
         moe_combine(y, self.topk_w, self.dest_pos, shared, self.out, stream)
 
     def expert_gate_up(self, weights: dict, stream=None):
+        self._rows_are(False, "expert_gate_up")
         act = MOE_ACT_SWIGLU_OAI if self.wl.ffn_act == "swiglu_oai" else MOE_ACT_SWIGLU
         moe_expert_gate_up(self.xs, self.offsets, weights["w1"], weights["w3"], self.h,
                            weights["b1"], weights["b3"], act, self.status, stream)
 
     def expert_down(self, weights: dict, stream=None):
+        self._rows_are(False, "expert_down")
         moe_expert_down(self.h, self.offsets, weights["w2"], self.y, weights["b2"], self.status,
                         stream)
 
     def norm(self, x, residual, gain, eps=1e-5, residual_out=None, stream=None):
         """The norm in front of the gate: self.xn, its MX rows self.x_mx, and the
         residual stream x + residual to residual_out."""
+        self._rows_are(True, "norm")
         moe_add_rmsnorm(x, residual, gain, eps, residual_out, self.xn, self.x_mx, stream)
         return self.xn
 
     def permute_mx(self, stream=None):
         """x_mx into expert order: elements and scales are byte rows to moe_permute."""
+        self._rows_are(True, "permute_mx")
         for src, dst in zip(self.x_mx.as_bf16_rows(), self.xs_mx.as_bf16_rows()):
             moe_permute(src, self.dest_pos, dst, stream)
 
     def expert_gate_up_mx(self, weights: dict, stream=None):
+        self._rows_are(True, "expert_gate_up_mx")
         act = MOE_ACT_SWIGLU_OAI if self.wl.ffn_act == "swiglu_oai" else MOE_ACT_SWIGLU
         moe_expert_gate_up_mx(self.xs_mx, self.offsets, weights["w1"], weights["w3"], self.h_mx,
                               weights["b1"], weights["b3"], act, self.status, stream)
 
     def expert_down_mx(self, weights: dict, stream=None):
+        self._rows_are(True, "expert_down_mx")
         moe_expert_down_mx(self.h_mx, self.offsets, weights["w2"], self.y, weights["b2"],
                            self.status, stream)
 
@@ -173,20 +185,29 @@ class RouterDispatch:
             self.permute(x, stream)
         else:
             self.permute_mx(stream)
-            self.expert_gate_up_mx(experts, stream)
-            self.expert_down_mx(experts, stream)
-            y = self.y
-        if experts is not None and self.mx is None:
-            self.expert_gate_up(experts, stream)
-            self.expert_down(experts, stream)
+        if experts is not None:
+            if self.mx is None:
+                self.expert_gate_up(experts, stream)
+                self.expert_down(experts, stream)
+            else:
+                self.expert_gate_up_mx(experts, stream)
+                self.expert_down_mx(experts, stream)
             y = self.y
         if self.wl.combine:
             self.combine(y, inputs["shared"], stream)
-        return self.out if self.wl.combine else (self.xs if self.mx is None else self.y)
+            return self.out
+        if self.mx is None:
+            return self.xs
+        return self.xs_mx if experts is None else self.y
 
     def run_hash_layer(self, inputs: dict, logits=None, stream=None):
-        """hash_route -> dispatch -> permute (the hash-routed layer's chain)."""
+        """hash_route -> dispatch -> permute (the hash-routed layer's chain); with MX
+        activations x is quantised in front of the permute."""
         self.hash_route(inputs["token_ids"], inputs["tid2eid"], logits, stream)
         self.dispatch(self.hash_ids, stream)
-        self.permute(inputs["x"], stream)
-        return self.xs
+        if self.mx is None:
+            self.permute(inputs["x"], stream)
+            return self.xs
+        moe_mx_quantize(inputs["x"], self.x_mx, stream)
+        self.permute_mx(stream)
+        return self.xs_mx
