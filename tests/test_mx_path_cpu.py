@@ -49,3 +49,12 @@ def test_no_ffn_shape():
     with pytest.raises(ValueError, match="no expert FFN"):
         RouterDispatch(dataclasses.replace(WORKLOADS["mixtral_tiny"], ffn_dim=0, T=4), device="cpu",
                        mx=moe.MOE_MX_E2M1)
+
+
+def test_inputs_that_would_go_unused_are_refused():
+    """A norm in front of bf16 rows, and a residual with no norm to add it in."""
+    x = torch.zeros((16, 8), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="norm"):
+        path_of(None).run({"x": x, "gain": x[0], "y": None, "w": None})
+    with pytest.raises(ValueError, match="residual"):
+        path_of(moe.MOE_MX_E4M3).run({"x": x, "residual": x, "y": None, "w": None})

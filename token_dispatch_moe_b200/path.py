@@ -166,10 +166,15 @@ class RouterDispatch:
         :func:`workloads.make_inputs`; without experts the combine reads the synthetic
         ``inputs["y"]``.  With MX activations, ``inputs["gain"]`` (and ``"residual"``,
         ``"residual_out"``, ``"eps"``) put the norm in front; without it x is quantised as
-        it is."""
+        it is.  A gain for bf16 rows, or a residual without a gain, is refused."""
         x = inputs["x"]
+        normed = inputs.get("gain") is not None
+        if normed:
+            self._rows_are(True, "norm")
+        elif self.mx is not None and inputs.get("residual") is not None:
+            raise ValueError("a residual without the norm's gain")
         if self.mx is not None:
-            if inputs.get("gain") is not None:
+            if normed:
                 x = self.norm(x, inputs.get("residual"), inputs["gain"], inputs.get("eps", 1e-5),
                               inputs.get("residual_out"), stream)
             else:
