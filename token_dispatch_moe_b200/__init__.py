@@ -141,8 +141,8 @@ def _stream(stream):
     A torch stream of another device than the current one is refused: the
     library launches on the current device, with its kernels reading the
     tensors' addresses there."""
-    if stream is None:  # the raw handle, without building a torch.cuda.Stream (3 us of a small call)
-        return torch._C._cuda_getCurrentRawStream(_current_device())
+    if stream is None:
+        return _current_stream(_current_device())
     s = stream
     if hasattr(s, "device") and s.device.index != torch.cuda.current_device():
         raise ValueError(f"stream is on {s.device}, the current device is "
@@ -155,8 +155,11 @@ def _check(status: int, where: str):
         raise MoeError(status, where)
 
 
-# The current device without the Python layers around it (a call here checks up to ten tensors).
+# The current device without the Python layers around it (a call here checks up to ten tensors),
+# and the current stream's handle without building a torch.cuda.Stream (3 us of a small call).
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def _need(t, dtype, name, ndim=None):
