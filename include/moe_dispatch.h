@@ -509,9 +509,11 @@ moe_status moe_mx_dequantize(const uint8_t *q, const uint8_t *scales, int64_t ro
  * x, residual, residual_out, y [T][d] bf16; gain [d] bf16; q, scales MX rows of
  * `format`.  residual_out (= h), y and q with scales are nullable, not all of
  * them.  residual_out may be residual or x, y may be x or residual (not both
- * outputs the same: refused).  8 <= d <= 16384, d % 8 == 0, eps >= 0.  The mean is
- * taken in fp32.  As the formula has it, a NaN makes its whole row of y NaN, an
- * infinity gives NaN in its place and zeros beside it.
+ * outputs the same: refused); nothing else may overlap.  8 <= d <= 16384, d % 8 == 0,
+ * eps >= 0.  The mean is taken in fp32: a row whose squares add up to more than its
+ * largest number (3.4e38) gives zeros, and squares below its smallest count as 0.  As the
+ * formula has it, a NaN makes its whole row of y NaN, an infinity gives NaN in its place
+ * and zeros beside it.
  */
 moe_status moe_add_rmsnorm(const moe_bf16_t *x, const moe_bf16_t *residual, const moe_bf16_t *gain,
                            float eps, int64_t T, int32_t d, moe_bf16_t *residual_out, moe_bf16_t *y,
@@ -530,7 +532,8 @@ moe_status moe_add_rmsnorm(const moe_bf16_t *x, const moe_bf16_t *residual, cons
  * rows of d values, [E][F] of them; b1, b3 [E][F] fp32, 16-byte aligned, or
  * NULL; h, h_scales: MX rows of F values, padding written.  Products are
  * exact and accumulate in fp32 on tcgen05 tensor cores; bias and activation
- * in fp32; one rounding, to h_format.  x_format, w_format, h_format: any.
+ * in fp32; one rounding, to h_format.  A sigmoid below 2^-126 (a gate below -87;
+ * clamped, below -51) counts as 0.  x_format, w_format, h_format: any.
  * d, F multiples of 8; E <= 4096.  Offsets that descend, are negative or
  * leave the rows report MOE_ERR_DEVICE_INDEX, and nothing is written.
  */

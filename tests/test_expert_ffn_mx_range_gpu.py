@@ -43,3 +43,16 @@ def test_gates_at_the_end_of_the_range(sign, fmt, act):
     # 2^-20 + 2^-22 * 11.9 for the clamped form.  On the far negative side the value is 0.
     rel = 2.0 ** -20 + 2.0 ** -22 * 11.9 if act == OAI else 2.0 ** -21
     check_h(h, want, rel * np.abs(want), slice(0, 3))
+
+
+@pytest.mark.parametrize("act", [SWIGLU, OAI])
+@pytest.mark.parametrize("up", [1.0, 7.0, 1e38])
+def test_gates_whose_sigmoid_counts_as_zero(up, act):
+    """Gates from -40 to -200 with ups of one size: a sigmoid below 2^-126 may count as 0."""
+    g = -np.linspace(40, 200, 96)
+    h, g, u = of_biases(g, np.full(96, up), act)
+    want = mo.activate(g, u, act == OAI)
+    factor = np.clip(u, -7.0, 7.0) + 1.0 if act == OAI else u
+    # what counts as 0, and the exponential's bound as in the other tests
+    bound = np.abs(g * factor) * 2.0 ** -126 + np.abs(want) * (2.0 ** -20 + 2.0 ** -22 * 1.702 * np.abs(g))
+    check_h(h, want, bound, slice(0, 3))
