@@ -57,6 +57,8 @@ constexpr int kXMaxE = 4096;
 constexpr int kXMaxDynamic = 227 * 1024 - 64;  // of a CTA on sm_100, without the static part
 constexpr int kXMaxCap = 224;  // tokens of a tile: two accumulators and the scales fill TMEM
 constexpr int kXMaxStages = 12;
+constexpr int kXSlots = 4;  // loads of scales in flight
+constexpr uint32_t kXWeightBytes = 128 * kXBK;  // a K block's weight tile in shared memory
 constexpr int kXBars = 512;  // bytes of barriers, the TMEM address and the tile ring
 constexpr int kXEpiThreads = 384;
 constexpr int kXParts = 3;          // warps that share a quarter of the TMEM lanes
@@ -70,6 +72,10 @@ constexpr int kXStageBytes[2] = {4 * kXParts * kXPart * 36 * 4, 2 * kXParts * kX
 constexpr float kXOaiAlpha = 1.702f;
 constexpr float kXOaiLimit = 7.0f;
 
+// Features of a CTA's tile: its 128 weight rows, halved where each feature has a gate and an up.
+template <bool GATE_UP>
+constexpr int kXFeatures = GATE_UP ? 64 : 128;
+
 struct MxFfnArgs {
     const int32_t *offsets;  // [E+1], ascending
     const float *bias0;      // gate_up: b1 [E][N]; down: b2 [E][N]
@@ -80,12 +86,10 @@ struct MxFfnArgs {
     int32_t *status;
     int64_t rows;
     int E, N;
-    int ft;                  // features of a CTA's tile
     int f_tiles;             // tiles (of a CTA or a pair) that cover the features
     int cap;                 // most tokens of a tile; also the columns of an accumulator
-    int num_kb, stages, slots, tmem_cols, act, h_fmt;
-    uint32_t a_bytes, b_bytes;     // a K block's weight and token tile in shared memory
-    uint32_t stage_bytes;          // both
+    int num_kb, stages, tmem_cols, act, h_fmt;
+    uint32_t stage_bytes;          // a K block's weight and token tile in shared memory
     uint32_t stage_tx, slot_tx;    // bytes their barriers count: 4-bit values packed
     uint32_t raw_b, tiled_b, slot_bytes, idesc;
     uint32_t sf, stg, bars, tables;  // offsets in shared memory (the stages come first)
@@ -206,10 +210,10 @@ struct Walk {
     int E, f_step, f_first, f_tiles, step_p, step_f;
     int p, f, e;
 
-    // ctas: CTAs that walk as one (1, or 2 of which this is number `rank`).
+    // ctas: CTAs that walk as one (1, or 2 of which this is number `rank`), each with `ft` features.
     __device__ __forceinline__ Walk(const MxFfnArgs &a, const int32_t *o, const int32_t *q,
-                                    int ctas, int rank)
-        : off(o), parts(q), E(a.E), f_step(ctas * a.ft), f_first(rank * a.ft), f_tiles(a.f_tiles) {
+                                    int ctas, int rank, int ft)
+        : off(o), parts(q), E(a.E), f_step(ctas * ft), f_first(rank * ft), f_tiles(a.f_tiles) {
         const int unit = (int)blockIdx.x / ctas, units = (int)gridDim.x / ctas;
         step_p = units / f_tiles;
         step_f = units - step_p * f_tiles;
@@ -328,13 +332,13 @@ __global__ void __launch_bounds__(kXThreads, 1)
                      const __grid_constant__ CUtensorMap map_xs, const MxFfnArgs a) {
     extern __shared__ __align__(16) uint8_t smem_mx[];
     __shared__ int abort_s;
-    constexpr int kCtas = PAIR ? 2 : 1;
+    constexpr int kCtas = PAIR ? 2 : 1, kFt = kXFeatures<GATE_UP>, R = kXSlots;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = PAIR ? (int)cluster_cta_rank() : 0;
     const uint32_t raw = smem_u32(smem_mx);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t *const gbase = smem_mx + (base - raw);
-    const int S = a.stages, R = a.slots;
+    const int S = a.stages;
     const uint32_t bar0 = base + a.bars;
     auto full_bar = [&](int s) { return bar0 + 8u * s; };                   // the leader's
     auto empty_bar = [&](int s) { return bar0 + 8u * (S + s); };
@@ -438,7 +442,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
             uint32_t filled = 0;
             bool ok = true;
             const uint32_t lead_full = PAIR ? cluster_map(full_bar(0), 0) : full_bar(0);
-            const uint32_t up = (uint32_t)a.ft * 128u;
+            constexpr uint32_t up = (uint32_t)kFt * kXBK;
             while (ok && !*abort_v) {
                 ok = tiles.take(w);
                 if (!ok || w.n == 0) break;
@@ -453,7 +457,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
                     if (rank == 0) mbar_arrive_expect_tx(full_bar(st.at), a.stage_tx);
                     load_tile<PAIR>(dst, &map_w0, bar, wrow, kb);
                     if (GATE_UP) load_tile<PAIR>(dst + up, &map_w1, bar, wrow, kb);
-                    load_tile<PAIR>(dst + a.a_bytes, &map_x, bar, xrow, kb);
+                    load_tile<PAIR>(dst + kXWeightBytes, &map_x, bar, xrow, kb);
                     st.next(S);
                     ++filled;
                 }
@@ -483,7 +487,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
             // descriptors: only the start address, in the low word, differs
             const uint64_t d0 = sw128_desc(base), s0 = scales_desc(base + a.sf + 2048u + a.raw_b);
             const uint32_t d_hi = (uint32_t)(d0 >> 32), s_hi = (uint32_t)(s0 >> 32);
-            const uint32_t a16 = a.a_bytes >> 4;
+            constexpr uint32_t a16 = kXWeightBytes >> 4;
             const uint32_t stage16 = a.stage_bytes >> 4, slot16 = a.slot_bytes >> 4;
             const uint32_t tiled16 = a.tiled_b >> 4;
             uint32_t d_lo = (uint32_t)d0, s_lo = (uint32_t)s0;  // of the ring places in use
@@ -561,7 +565,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
                     const uint32_t bar = raw_bar(sf.at);
                     mbar_arrive_expect_tx(bar, a.slot_tx);
                     tma_load_2d(sl, &map_w0s, bar, 4 * c, wrow);
-                    if (GATE_UP) tma_load_2d(sl + (uint32_t)a.ft * 16u, &map_w1s, bar, 4 * c, wrow);
+                    if (GATE_UP) tma_load_2d(sl + (uint32_t)kFt * 16u, &map_w1s, bar, 4 * c, wrow);
                     tma_load_2d(sl + 2048u, &map_xs, bar, 4 * c, w.row0);
                     sf.next(R);
                     ++filled;
@@ -612,7 +616,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
         if (!ok) *abort_v = 1;
     } else if (warp == 16) {
         if (lane == 0) {
-            Walk walk(a, off, parts, kCtas, rank);
+            Walk walk(a, off, parts, kCtas, rank, kFt);
             Tile w;
             Ring to;
             for (bool any = true; any && !*abort_v; walk.next(), to.next(kXTiles)) {
@@ -629,21 +633,19 @@ __global__ void __launch_bounds__(kXThreads, 1)
         // Three warps share a quarter of the TMEM lanes, a third of a chunk's token columns each
         // (with two the epilogue's latencies held up tiles of few K blocks: qwen3 gate_up 390
         // against 376 us, 509 ragged rows' down 108 against 103).
-        // gate_up: the 32 gate features of quarter q and the same up features, ft / 32 quarters
+        // gate_up: the 32 gate features of quarter q and the same up features, two quarters
         // on, are an MX block; the two warps that hold them meet in a staging buffer of their
         // own.  down: a warp's 32 features are its own affair.
         const int q = warp & 3, part = (warp - 4) >> 2;
-        const int quarters = (GATE_UP ? 2 : 1) * a.ft / 32, up = a.ft / 32;
-        const bool works = q < quarters;
-        const int duo = GATE_UP ? q % up : q;  // block of 32 features
-        const int member = GATE_UP && q >= up ? 1 : 0;
+        const int duo = GATE_UP ? q & 1 : q;  // block of 32 features
+        const int member = GATE_UP ? q >> 1 : 0;
         const int bar_id = 2 + kXParts * duo + part;
         constexpr int kPitch = kXPitch[GATE_UP];
         float *stg = reinterpret_cast<float *>(gbase + a.stg) +
                      (kXParts * duo + part) * (kXPart * kPitch);
         Ring acc;
         const int grp = lane & 3;  // 8 of the block's features
-        const int cover = a.f_tiles * kCtas * a.ft;  // features of all tiles, N or a little more
+        const int cover = a.f_tiles * kCtas * kFt;  // features of all tiles, N or a little more
         const uint32_t lead_tempty = PAIR ? cluster_map(tempty_bar(0), 0) : tempty_bar(0);
         for (;;) {
             // One thread polls; the others wait at the barrier that carries its answer.
@@ -672,13 +674,13 @@ __global__ void __launch_bounds__(kXThreads, 1)
             const bool real_f = f < a.N;
             const int mine = w.n - kXPart * part;  // tokens from this part's first on
             uint32_t v[kXPart];
-            if (works && mine > 0) tmem_ld16_nowait(trow, v);
+            if (mine > 0) tmem_ld16_nowait(trow, v);
             f32x2 b0[4], b1[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) b0[k] = b1[k] = 0ull;
             if (real_f && a.bias0) load8(a.bias0 + (int64_t)w.e * a.N + f, b0);
             if (GATE_UP && real_f && a.bias1) load8(a.bias1 + (int64_t)w.e * a.N + f, b1);
-            for (int c0 = 0; works && c0 < mine; c0 += kXChunk) {
+            for (int c0 = 0; c0 < mine; c0 += kXChunk) {
                 auto meet = [&] {  // the warps that share the buffer
                     if (GATE_UP)
                         asm volatile("bar.sync %0, 64;" ::"r"(bar_id) : "memory");
@@ -727,7 +729,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
                 }
             }
             // The buffer's last readers before the next tile's writers.
-            if (GATE_UP && works && mine > 0) asm volatile("bar.sync %0, 64;" ::"r"(bar_id) : "memory");
+            if (GATE_UP && mine > 0) asm volatile("bar.sync %0, 64;" ::"r"(bar_id) : "memory");
             // This warp's reads are done: the accumulator is free for the tile after next.
             tc_fence_before();
             __syncwarp();
@@ -738,7 +740,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
                     mbar_arrive(tempty_bar(acc.at));
             }
             // The last feature tile's tokens get what is left of their rows' padding.
-            if (GATE_UP && w.f0 + a.ft == cover) {
+            if (GATE_UP && w.f0 + kFt == cover) {
                 for (int i = (int)threadIdx.x - 128; i < w.n; i += kXEpiThreads) {
                     const int64_t row = (int64_t)w.row0 + i;
                     uint8_t *qrow = a.hq + row * a.h_row, *srow = a.hs + row * a.h_scale;
@@ -775,17 +777,16 @@ template <bool GATE_UP, bool PAIR>
 moe_status launch_expert_mx(const uint8_t *xq, const uint8_t *xs, int32_t x_fmt, const uint8_t *w0,
                             const uint8_t *w0s, const uint8_t *w1, const uint8_t *w1s,
                             int32_t w_fmt, int32_t K, MxFfnArgs a, moe_stream_t stream) {
-    constexpr int kCtas = PAIR ? 2 : 1;
+    constexpr int kCtas = PAIR ? 2 : 1, kFt = kXFeatures<GATE_UP>;
     const bool w4 = w_fmt == MOE_MX_E2M1, x4 = x_fmt == MOE_MX_E2M1;
-    a.f_tiles = (a.N + kCtas * a.ft - 1) / (kCtas * a.ft);
+    a.f_tiles = (a.N + kCtas * kFt - 1) / (kCtas * kFt);
     a.num_kb = mx_padded(K) / kXBK;
-    const int a_rows = (GATE_UP ? 2 : 1) * a.ft, b_rows = a.cap / kCtas;
-    a.a_bytes = (uint32_t)a_rows * 128u;
-    a.b_bytes = (uint32_t)b_rows * 128u;
-    a.stage_bytes = a.a_bytes + a.b_bytes;
-    a.stage_tx = (uint32_t)kCtas *
-                 ((w4 ? a.a_bytes / 2 : a.a_bytes) + (x4 ? a.b_bytes / 2 : a.b_bytes));
-    a.slot_tx = (uint32_t)(a_rows + a.cap) * 16u;
+    const int b_rows = a.cap / kCtas;
+    const uint32_t b_bytes = (uint32_t)b_rows * kXBK;
+    a.stage_bytes = kXWeightBytes + b_bytes;
+    a.stage_tx =
+        (uint32_t)kCtas * ((w4 ? kXWeightBytes / 2 : kXWeightBytes) + (x4 ? b_bytes / 2 : b_bytes));
+    a.slot_tx = (uint32_t)(128 + a.cap) * 16u;
     a.raw_b = a.cap > 128 ? 4096u : 2048u;
     a.tiled_b = a.cap > 128 ? 1024u : 512u;
     a.slot_bytes = 2048u + a.raw_b + 2048u + 4u * a.tiled_b;
@@ -795,16 +796,14 @@ moe_status launch_expert_mx(const uint8_t *xq, const uint8_t *xs, int32_t x_fmt,
     a.tmem_cols = cols;
     const uint32_t stg = kXStageBytes[GATE_UP], bars = kXBars;
     const uint32_t tables = ((uint32_t)(2 * (a.E + 1)) * 4u + 15u) / 16u * 16u;
-    // 1024: alignment slack; MMAs read 128 weight rows where a tile has fewer: what lies behind
-    // the stages is large enough for that
-    const int64_t rest =
-        (int64_t)kXMaxDynamic - 1024 - stg - bars - tables - (int64_t)a.slots * a.slot_bytes;
+    const int64_t rest = (int64_t)kXMaxDynamic - 1024 /* alignment slack */ - stg - bars - tables -
+                         (int64_t)kXSlots * a.slot_bytes;
     int64_t stages = rest / a.stage_bytes;
     if (stages > kXMaxStages) stages = kXMaxStages;
     if (stages < 2) return MOE_ERR_UNSUPPORTED;
     a.stages = (int)stages;
     a.sf = (uint32_t)a.stages * a.stage_bytes;
-    a.stg = a.sf + (uint32_t)a.slots * a.slot_bytes;
+    a.stg = a.sf + (uint32_t)kXSlots * a.slot_bytes;
     a.bars = a.stg + stg;
     a.tables = a.bars + bars;
     const size_t smem = 1024 + (size_t)a.tables + tables;
@@ -812,15 +811,15 @@ moe_status launch_expert_mx(const uint8_t *xq, const uint8_t *xs, int32_t x_fmt,
     CUtensorMap mw0, mw1, mw0s, mw1s, mx, mxs;
     const int64_t wrows = (int64_t)a.E * a.N;
     const int64_t Kp = mx_padded(K), sp = mx_scale_bytes(K);
-    if (!make_mx_map(&mw0, w0, wrows, Kp, w4, a.ft) ||
-        !make_byte_map(&mw0s, w0s, wrows, sp, a.ft) ||
+    if (!make_mx_map(&mw0, w0, wrows, Kp, w4, kFt) ||
+        !make_byte_map(&mw0s, w0s, wrows, sp, kFt) ||
         !make_mx_map(&mx, xq, a.rows, Kp, x4, b_rows) ||
         !make_byte_map(&mxs, xs, a.rows, sp, a.cap))
         return MOE_ERR_CUDA;
     mw1 = mw0;
     mw1s = mw0s;
-    if (GATE_UP && (!make_mx_map(&mw1, w1, wrows, Kp, w4, a.ft) ||
-                    !make_byte_map(&mw1s, w1s, wrows, sp, a.ft)))
+    if (GATE_UP && (!make_mx_map(&mw1, w1, wrows, Kp, w4, kFt) ||
+                    !make_byte_map(&mw1s, w1s, wrows, sp, kFt)))
         return MOE_ERR_CUDA;
     // Never more CTAs than the most tiles these rows can make.
     const int64_t parts = a.rows / a.cap + (a.rows < a.E ? a.rows : a.E);
@@ -846,7 +845,7 @@ moe_status launch_expert_mx(const uint8_t *xq, const uint8_t *xs, int32_t x_fmt,
 // Tile shape by the rows an expert has on average.  The token tile should just hold them, and
 // their spread (1.4 of its standard deviation: routing is near a draw), in as few equal parts
 // as fit: wider, it takes shared memory from the weights in flight and loads tokens that are
-// not there (both boxes are cap rows); narrower, more blocks are cut into parts, each of which
+// not there (a tile's boxes hold cap rows, however few it has); narrower, more blocks are cut into parts, each of which
 // reads the weights again.  From 33 rows on pairs of CTAs, each with half of the tokens' bytes.
 // Measured with 128 experts of 2880 x 2880, e2m1 weights, gate_up in us, by rows an expert:
 //    8, 20, 32 (one CTA):  cap 16: 189 289 393,  32: 197 203 261,  48: -   202 211,  64: 217 218 238
@@ -862,8 +861,6 @@ moe_status run_expert_mx(const uint8_t *xq, const uint8_t *xs, int32_t x_fmt, co
     const double need = (double)share + 1.4 * sqrt((double)share);
     const double parts = ceil(need / kXMaxCap);
     a.cap = ((int)ceil(need / parts) + 15) / 16 * 16;
-    a.ft = GATE_UP ? 64 : 128;
-    a.slots = 4;
     if (share <= 32)
         return launch_expert_mx<GATE_UP, false>(xq, xs, x_fmt, w0, w0s, w1, w1s, w_fmt, K, a,
                                                 stream);
