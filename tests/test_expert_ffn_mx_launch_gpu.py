@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import token_dispatch_moe_b200 as moe
-from test_expert_ffn_mx_gpu import DEV, E2, E4, blocks, f64, mx_of, randn
+from test_expert_ffn_mx_gpu import DEV, E2, E4, blocks, f64, filled, mx_of, randn
 import mx_oracle as mo
 import numpy as np
 
@@ -65,6 +65,26 @@ def test_pairs_close_together():
         torch.cuda.synchronize()
         for c in calls:
             c.check()
+
+
+@pytest.mark.parametrize("off,status", [
+    ([0, 0, 0], moe.MOE_OK), ([200, 200, 200], moe.MOE_OK), ([7, 7, 7], moe.MOE_OK),
+    ([0, 150, 100], moe.MOE_ERR_DEVICE_INDEX), ([-8, 100, 200], moe.MOE_ERR_DEVICE_INDEX),
+    ([0, 100, 201], moe.MOE_ERR_DEVICE_INDEX)])
+def test_pairs_without_tiles(off, status):
+    """Pairs that find no row, or offsets to report: they end, and write nothing."""
+    E, d, F, rows = 2, 128, 72, 200
+    offsets = torch.tensor(off, dtype=torch.int32, device=DEV)
+    xs, w1, w2 = mx_of(randn((rows, d), 1), E4), mx_of(randn((E, F, d), 2), E2), mx_of(randn((E, d, F), 3), E2)
+    h, hin = filled((rows,), F, E4), mx_of(randn((rows, F), 4), E4)
+    y = torch.full((rows, d), 9.0, dtype=torch.bfloat16, device=DEV)
+    for call in (lambda st: moe.moe_expert_gate_up_mx(xs, offsets, w1, w1, h, d_status=st),
+                 lambda st: moe.moe_expert_down_mx(hin, offsets, w2, y, d_status=st)):
+        st = torch.zeros((1,), dtype=torch.int32, device=DEV)
+        call(st)
+        torch.cuda.synchronize()
+        assert st.item() == status
+    assert (h.q == 0xA5).all() and (h.scales == 0xA5).all() and (y == 9.0).all()
 
 
 @pytest.mark.parametrize("shapes", [
