@@ -525,7 +525,7 @@ moe_status moe_add_rmsnorm(const moe_bf16_t *x, const moe_bf16_t *residual, cons
  * with e the expert whose block [offsets[e], offsets[e+1]) holds row r.  The
  * blocks are ragged: offsets as moe_dispatch writes them (or padded ones; the
  * rows between are rows like any other).  No row outside the blocks is read
- * into a result or written.
+ * into a result or written.  h overlaps no operand.
  * The tile shape goes by rows / E: where the rows in use are known to be
  * fewer than a buffer holds, pass their number.
  * xq, xs: MX rows of d values, `rows` of them; w1, w3 (and their scales): MX
@@ -549,8 +549,8 @@ moe_status moe_expert_gate_up_mx(const uint8_t *xq, const uint8_t *xs, int32_t x
  * moe_expert_down_mx -- y[r] = bf16( h[r] . W2[e]^T + b2[e] )
  * h, h_scales: MX rows of F values; w2, w2_scales: MX rows of F values, [E][d]
  * of them; b2 [E][d] fp32, 16-byte aligned, or NULL; y [rows][d] bf16 (the
- * expert outputs moe_combine reads).  Blocks, limits and status as
- * moe_expert_gate_up_mx.
+ * expert outputs moe_combine reads).  y overlaps no operand.  Blocks, limits and
+ * status as moe_expert_gate_up_mx.
  */
 moe_status moe_expert_down_mx(const uint8_t *h, const uint8_t *h_scales, int32_t h_format,
                               const int32_t *offsets, const uint8_t *w2, const uint8_t *w2_scales,

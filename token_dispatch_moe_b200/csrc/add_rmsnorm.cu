@@ -10,8 +10,8 @@
 // was fused.  The MX rows are made of the rounded y: the gate and the experts
 // see one and the same row, and the bits are moe_mx_quantize's on y.
 //
-// One pass, bound by memory (9.03 bytes a value with every output; 65,536 x
-// 7168: 630 us, 6.7 TB/s; 16,384 x 2048: 48 us, 6.3 TB/s): a row's
+// One pass, bound by memory (9.03 bytes a value with every output, e4m3: 65,536
+// x 7168 625 to 640 us, 6.7 TB/s; 16,384 x 2048 48 us, 6.3 TB/s): a row's
 // threads keep it in registers between the sum of squares and the outputs.
 // Rows of more than 1024 values have a block of threads each; narrower ones
 // a warp, or half a warp up to 128 values, 8 or 16 rows a block (65,536 x 128:
@@ -37,8 +37,9 @@ struct NormArgs {
 
 // (sum / d + eps)^(-1/2) within one unit of fp32: the quotient by one step on the remainder, the
 // root by one Newton step on the hardware's estimate with the residual 1 - v y^2 kept whole.
-// Every thread takes it, so the divide and square root sequences would cost (2880 wide: 268
-// against 317 us); and an error of the row's factor moves a whole row's roundings.
+// Every thread takes it, so the divide and square root sequences would cost (65,536 x 2880, every
+// output, e2m1: 288 against 267 us); and an error of the row's factor moves a whole row's
+// roundings.
 __device__ __forceinline__ float inverse_root(float sum, float d, float inv_d, float eps) {
     float v = sum * inv_d;
     if (v < __int_as_float(0x7f800000)) v = fmaf(fmaf(-v, d, sum), inv_d, v);  // not of inf or NaN
@@ -149,8 +150,10 @@ cudaError_t launch_norm(const NormArgs &a, cudaStream_t s) {
         if (vecs <= 64) return launch_pdl(add_rmsnorm_kernel<2, FMT, 32>, grid, block, 0, s, a);
         return launch_pdl(add_rmsnorm_kernel<4, FMT, 32>, grid, block, 0, s, a);
     }
-    // The fewest vectors a thread, two at least, with which a row fits 256 threads (16,384 x
-    // 2048 with one: 49 us, with two 46; 65,536 x 7168 with four: 588, with eight 639).
+    // The fewest vectors a thread, two at least, with which a row fits 256 threads.  Every
+    // output, e2m1: 16,384 x 2048 with one 49 us, two 46, eight 51; 65,536 x 7168 with four 627,
+    // eight 719; 65,536 x 2880 with two 268, eight 345.  Without MX rows the same but at 7168
+    // (four 575, eight 550).
     int vpt = 2;
     while (vpt * 256 < vecs) vpt *= 2;
     const dim3 grid((unsigned)a.T), block((unsigned)(((vecs + vpt - 1) / vpt + 31) / 32 * 32));

@@ -34,7 +34,7 @@
 // Every wait is bounded, as in the bf16 kernels.
 //
 // What bounds it.  Few rows: the weights' bytes (128 experts of 2880 x 2880, 64
-// tokens of 4 slots: gate_up 158 to 164 us for 0.98 GB, 6.0 to 6.2 TB/s).  Inside an SM a K
+// tokens of 4 slots: gate_up 158 to 166 us for 0.98 GB, 5.9 to 6.2 TB/s).  Inside an SM a K
 // block costs 32 KB of shared memory traffic (16 KB of widened weights written
 // and read), 256 clocks at least and 290 measured, under HBM's share.  Many
 // rows: tensor pipe, L2 reads and the power cap together (131,072 rows: gate_up

@@ -31,6 +31,9 @@ class RouterDispatch:
         separate route kernel spread over the whole GPU.)
         keep_logits: also write the logits (parity checks need them; the fused
         path skips them otherwise).
+        n_rows: rows of the permuted buffers, at least the assignments of every batch (default:
+        T * k_max, or the limited dispatch's bound).  The MX products size their tiles by it:
+        where tokens take fewer than k_max experts, give the number in use.
         mx: microscaled format (MOE_MX_E4M3, MOE_MX_E2M1) of the activations; the
         experts' FFN then takes MX operands (weights as make_mx_expert_weights
         lays them out), over the dispatch's blocks as they are."""
